@@ -327,6 +327,108 @@ typedef struct {
 int iskv_decode_attn_noalloc(const iskv_decode_view *view, const float *q_dev, float *out_dev,
                              iskv_stream_t stream);
 
+/*
+ * ---- Exact caches --------------------------------------------------------------------------
+ * Attention over rows that are kept as they are (the prompt before it is compressed, a cache that
+ * is bounded by a window or by eviction instead of by its rank, samples that share a prompt), in
+ * caller-owned memory. These calls keep no state and allocate nothing: the caller passes a
+ * workspace of at least the size that the *_workspace() call of the same arguments gives (16-byte
+ * aligned, contents irrelevant before and after). Calls whose work can overlap on the GPU need
+ * workspaces of their own; that goes for two captured graphs that are replayed at the same time.
+ * They run on the current CUDA device, which has to own all the pointers, and are capturable.
+ *
+ * Keys are as attended (already rotated), scores have the scale 1/sqrt(128), the softmax is exact,
+ * q-head g reads kv-head g / (n_q/n_kv), and a query that sees no row gives zeros. Rows that no
+ * query of their sequence sees are not used: they may hold anything, NaN included. Device arrays
+ * of lengths are read on the device: values below 0 count as 0, values above the capacity as the
+ * capacity. Strides count elements, have to be multiples of 16 bytes and may be 0 where rows or
+ * queries are shared (never in outputs); a stride over an extent of 1 is not read.
+ */
+typedef struct {
+    const void *k, *v;       /* element (b, h, j, c) at b seq + h head + j row + c; 16-byte aligned */
+    long long seq_stride, head_stride, row_stride;
+    int batch, n_kv_heads;   /* batch * n_kv_heads <= 65535                                      */
+    int rows;                /* capacity per sequence (0 .. 2^24; 0: k and v are not read)         */
+    int dtype;               /* ISKV_BF16 or ISKV_F32                                             */
+    const int *lens;         /* device, [batch]: rows held by each sequence; NULL: `rows`          */
+} iskv_exact_rows;
+
+typedef struct {
+    const void *q;           /* element (b, g, i, c) at b seq + g head + i tok + c; 16-byte aligned */
+    void *out;               /* the same with the o_ strides                                      */
+    long long q_seq_stride, q_head_stride, q_tok_stride;
+    long long o_seq_stride, o_head_stride, o_tok_stride;
+    int n_q_heads;           /* n_kv_heads times 1 .. 8                                           */
+    int m;                   /* query tokens per sequence (capacity)                              */
+    int dtype;               /* of q and out: ISKV_BF16 or ISKV_F32 (float32 rows: ISKV_F32 only,  */
+                             /* else ISKV_ERR_UNSUPPORTED)                                       */
+    const int *q_lens;       /* device, [batch]: tokens of each sequence; NULL: m                 */
+} iskv_exact_queries;
+
+typedef struct {
+    const void *k, *v;       /* element (h, j, c) at h head + j row + c; the rows' dtype           */
+    long long head_stride, row_stride;
+    int rows;                /* 0 .. 2^24                                                        */
+} iskv_exact_prefix;
+
+/*
+ * Attention with a sliding window and a few first tokens that stay visible. The last q_lens[b] of a
+ * sequence's lens[b] rows are the call's tokens: token i sits at p = lens[b] - q_lens[b] + i and
+ * sees the rows j <= p with j < sinks or j > p - window (window >= lens: causal attention). From
+ * a whole prompt (m = rows) to single tokens (m = 1). Outputs of tokens i >= q_lens[b] are not
+ * written. A token's own row has to be in the cache before the call.
+ * Where tokens see different rows of a call, a row that is not finite may reach every token
+ * within 64 positions of one that sees it.
+ * Errors: ISKV_ERR_INVALID_ARG, ISKV_ERR_UNSUPPORTED, ISKV_ERR_CAPACITY (workspace too small),
+ *         ISKV_ERR_CUDA.
+ */
+int iskv_window_attn(const iskv_exact_rows *rows, const iskv_exact_queries *q, int window,
+                     int sinks, void *ws, size_t ws_bytes, iskv_stream_t stream);
+int iskv_window_attn_workspace(const iskv_exact_rows *rows, const iskv_exact_queries *q,
+                               int window, int sinks, size_t *bytes_out);
+
+/*
+ * Decode attention of one token per sequence (m = 1, q_lens = NULL) over all rows of its sequence,
+ * which also accumulates the rows' attention weights:
+ *   mass_out[b][h][j] = mass[b][h][j] + sum over the q-heads g of kv-head h of softmax_j(s_g)
+ * for j < lens[b]; the other entries are not written. mass, mass_out: fp32 [batch][n_kv][rows];
+ * they may be the same array, or not overlap.
+ * Errors: as iskv_window_attn().
+ */
+int iskv_mass_decode(const iskv_exact_rows *rows, const iskv_exact_queries *q, const float *mass,
+                     float *mass_out, void *ws, size_t ws_bytes, iskv_stream_t stream);
+int iskv_mass_decode_workspace(const iskv_exact_rows *rows, const iskv_exact_queries *q,
+                               size_t *bytes_out);
+
+/*
+ * Eviction: every (sequence, kv-head) that holds more than `budget` rows keeps that many, in its
+ * slots 0 .. budget - 1. It keeps the rows of positions < sinks, the rows whose position is among
+ * the `recent` last up to its largest one, and the heaviest of the others (ties: the lowest slot;
+ * a NaN counts as heaviest). Kept rows of slots >= budget move into the freed slots below it, both
+ * in ascending order; the other rows stay where they are, so slots are in no order of positions.
+ * k and v are moved in place. mass fp32 and pos int32, [batch][n_kv][rows], hold each row's weight
+ * and position (distinct within a kv-head); mass_out, pos_out and lens_out (device, [batch]) get
+ * what the kept rows have, entries behind them are not written. Each may be its input (in place)
+ * or not overlap it. sinks + recent <= budget.
+ * Errors: as iskv_window_attn().
+ */
+int iskv_evict(const iskv_exact_rows *rows, const float *mass, float *mass_out, const int *pos,
+               int *pos_out, int *lens_out, int budget, int recent, int sinks, void *ws,
+               size_t ws_bytes, iskv_stream_t stream);
+int iskv_evict_workspace(const iskv_exact_rows *rows, int budget, size_t *bytes_out);
+
+/*
+ * Decode attention of one token per sequence (m = 1, q_lens = NULL) over a prefix that the whole
+ * batch shares, and then its sequence's own rows (capacity 0 allowed). The prefix's keys and values
+ * are read once for a group of sequences, not once per sequence.
+ * Errors: as iskv_window_attn().
+ */
+int iskv_prefix_decode(const iskv_exact_rows *rows, const iskv_exact_queries *q,
+                       const iskv_exact_prefix *prefix, void *ws, size_t ws_bytes,
+                       iskv_stream_t stream);
+int iskv_prefix_decode_workspace(const iskv_exact_rows *rows, const iskv_exact_queries *q,
+                                 const iskv_exact_prefix *prefix, size_t *bytes_out);
+
 /* Static description of an error code. */
 const char *iskv_strerror(int code);
 

@@ -3,7 +3,8 @@ over the compressed history, served by hand-written sm_100a CUDA kernels behind 
 (``include/iskv.h``, ``libiskv.so``).
 
 ``binding`` mirrors the C entry points one to one; ``cache.IsKVCache`` is a thin owner of a handle
-that allocates caller-side buffers with torch. Importing the package loads ``libiskv.so`` and
+that allocates caller-side buffers with torch. ``exact.ExactKVCache`` is attention over exact rows
+in the caller's tensors (window with sinks, accumulated weights and eviction, shared prefix). Importing the package loads ``libiskv.so`` and
 raises if it has not been built.
 """
 from .binding import *  # noqa: F401,F403
@@ -14,4 +15,7 @@ def __getattr__(name):
     if name == "IsKVCache":
         from .cache import IsKVCache
         return IsKVCache
+    if name == "ExactKVCache":
+        from .exact import ExactKVCache
+        return ExactKVCache
     raise AttributeError(name)

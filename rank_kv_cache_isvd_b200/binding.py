@@ -23,6 +23,10 @@ __all__ = [
     "iskv_join", "iskv_append_decode",
     "iskv_decode_view", "iskv_decode_attn_noalloc", "ISKV_NOALLOC_SCRATCH_FLOATS",
     "iskv_protect", "iskv_prefill",
+    "iskv_exact_rows", "iskv_exact_queries", "iskv_exact_prefix",
+    "iskv_window_attn", "iskv_window_attn_workspace", "iskv_mass_decode",
+    "iskv_mass_decode_workspace", "iskv_evict", "iskv_evict_workspace", "iskv_prefix_decode",
+    "iskv_prefix_decode_workspace",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libiskv.so")
@@ -102,6 +106,51 @@ class iskv_decode_view(ctypes.Structure):
     ]
 
 
+class iskv_exact_rows(ctypes.Structure):
+    """Rows of an exact cache (mirrors the C struct)."""
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("seq_stride", ctypes.c_longlong),
+        ("head_stride", ctypes.c_longlong),
+        ("row_stride", ctypes.c_longlong),
+        ("batch", ctypes.c_int),
+        ("n_kv_heads", ctypes.c_int),
+        ("rows", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("lens", ctypes.c_void_p),
+    ]
+
+
+class iskv_exact_queries(ctypes.Structure):
+    """Queries and outputs of a call on an exact cache (mirrors the C struct)."""
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("q_seq_stride", ctypes.c_longlong),
+        ("q_head_stride", ctypes.c_longlong),
+        ("q_tok_stride", ctypes.c_longlong),
+        ("o_seq_stride", ctypes.c_longlong),
+        ("o_head_stride", ctypes.c_longlong),
+        ("o_tok_stride", ctypes.c_longlong),
+        ("n_q_heads", ctypes.c_int),
+        ("m", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("q_lens", ctypes.c_void_p),
+    ]
+
+
+class iskv_exact_prefix(ctypes.Structure):
+    """Rows that every sequence shares (mirrors the C struct)."""
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("head_stride", ctypes.c_longlong),
+        ("row_stride", ctypes.c_longlong),
+        ("rows", ctypes.c_int),
+    ]
+
+
 class IsKVError(RuntimeError):
     def __init__(self, code: int, what: str = ""):
         self.code = code
@@ -112,6 +161,7 @@ class IsKVError(RuntimeError):
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _ll = ctypes.c_longlong
+_sz = ctypes.c_size_t
 
 _SIGNATURES = {
     "iskv_create": (_i, [ctypes.POINTER(iskv_config), ctypes.POINTER(_vp)]),
@@ -134,6 +184,14 @@ _SIGNATURES = {
                              ctypes.POINTER(_ll)]),
     "iskv_decode_attn_noalloc": (_i, [ctypes.POINTER(iskv_decode_view), _vp, _vp, _vp]),
     "iskv_prefill": (_i, [_vp, _i, _vp, _vp, _ll, ctypes.POINTER(iskv_protect), _vp]),
+    "iskv_window_attn": (_i, [_vp, _vp, _i, _i, _vp, _sz, _vp]),
+    "iskv_window_attn_workspace": (_i, [_vp, _vp, _i, _i, ctypes.POINTER(_sz)]),
+    "iskv_mass_decode": (_i, [_vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "iskv_mass_decode_workspace": (_i, [_vp, _vp, ctypes.POINTER(_sz)]),
+    "iskv_evict": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _sz, _vp]),
+    "iskv_evict_workspace": (_i, [_vp, _i, ctypes.POINTER(_sz)]),
+    "iskv_prefix_decode": (_i, [_vp, _vp, _vp, _vp, _sz, _vp]),
+    "iskv_prefix_decode_workspace": (_i, [_vp, _vp, _vp, ctypes.POINTER(_sz)]),
 }
 
 
@@ -278,3 +336,58 @@ def iskv_prefill(handle, layer: int, k_rows, v_rows, T0: int, protect=None, stre
     """``protect``: an :class:`iskv_protect` or ``None`` (no protection)."""
     return lib.iskv_prefill(handle, layer, _ptr(k_rows), _ptr(v_rows), T0,
                             None if protect is None else ctypes.byref(protect), _stream(stream))
+
+
+def _ref(x):
+    """Address of a C struct, or None. The calls below read it before they return."""
+    return None if x is None else ctypes.addressof(x)
+
+
+def iskv_window_attn(rows, q, window: int, sinks: int, ws, ws_bytes: int, stream=None) -> int:
+    return lib.iskv_window_attn(_ref(rows), _ref(q), window, sinks, _ptr(ws), ws_bytes,
+                                _stream(stream))
+
+
+def iskv_window_attn_workspace(rows, q, window: int, sinks: int):
+    """Returns ``(code, bytes)``."""
+    n = _sz(0)
+    code = lib.iskv_window_attn_workspace(_ref(rows), _ref(q), window, sinks, ctypes.byref(n))
+    return code, n.value
+
+
+def iskv_mass_decode(rows, q, mass, mass_out, ws, ws_bytes: int, stream=None) -> int:
+    return lib.iskv_mass_decode(_ref(rows), _ref(q), _ptr(mass), _ptr(mass_out), _ptr(ws),
+                                ws_bytes, _stream(stream))
+
+
+def iskv_mass_decode_workspace(rows, q):
+    """Returns ``(code, bytes)``."""
+    n = _sz(0)
+    code = lib.iskv_mass_decode_workspace(_ref(rows), _ref(q), ctypes.byref(n))
+    return code, n.value
+
+
+def iskv_evict(rows, mass, mass_out, pos, pos_out, lens_out, budget: int, recent: int, sinks: int,
+               ws, ws_bytes: int, stream=None) -> int:
+    return lib.iskv_evict(_ref(rows), _ptr(mass), _ptr(mass_out), _ptr(pos), _ptr(pos_out),
+                          _ptr(lens_out), budget, recent, sinks, _ptr(ws), ws_bytes,
+                          _stream(stream))
+
+
+def iskv_evict_workspace(rows, budget: int):
+    """Returns ``(code, bytes)``."""
+    n = _sz(0)
+    code = lib.iskv_evict_workspace(_ref(rows), budget, ctypes.byref(n))
+    return code, n.value
+
+
+def iskv_prefix_decode(rows, q, prefix, ws, ws_bytes: int, stream=None) -> int:
+    return lib.iskv_prefix_decode(_ref(rows), _ref(q), _ref(prefix), _ptr(ws), ws_bytes,
+                                  _stream(stream))
+
+
+def iskv_prefix_decode_workspace(rows, q, prefix):
+    """Returns ``(code, bytes)``."""
+    n = _sz(0)
+    code = lib.iskv_prefix_decode_workspace(_ref(rows), _ref(q), _ref(prefix), ctypes.byref(n))
+    return code, n.value
