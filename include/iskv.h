@@ -429,6 +429,13 @@ int iskv_prefix_decode(const iskv_exact_rows *rows, const iskv_exact_queries *q,
 int iskv_prefix_decode_workspace(const iskv_exact_rows *rows, const iskv_exact_queries *q,
                                  const iskv_exact_prefix *prefix, size_t *bytes_out);
 
+/*
+ * Synchronises `stream` and returns the sticky status of the calls on exact caches on the current
+ * device since the last such query: ISKV_OK, or ISKV_ERR_TIMEOUT when a device-side wait of one of
+ * them hit its bound (its outputs are then incomplete), or ISKV_ERR_CUDA.
+ */
+int iskv_exact_status(iskv_stream_t stream);
+
 /* Static description of an error code. */
 const char *iskv_strerror(int code);
 

@@ -26,7 +26,7 @@ __all__ = [
     "iskv_exact_rows", "iskv_exact_queries", "iskv_exact_prefix",
     "iskv_window_attn", "iskv_window_attn_workspace", "iskv_mass_decode",
     "iskv_mass_decode_workspace", "iskv_evict", "iskv_evict_workspace", "iskv_prefix_decode",
-    "iskv_prefix_decode_workspace",
+    "iskv_prefix_decode_workspace", "iskv_exact_status",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libiskv.so")
@@ -192,6 +192,7 @@ _SIGNATURES = {
     "iskv_evict_workspace": (_i, [_vp, _i, ctypes.POINTER(_sz)]),
     "iskv_prefix_decode": (_i, [_vp, _vp, _vp, _vp, _sz, _vp]),
     "iskv_prefix_decode_workspace": (_i, [_vp, _vp, _vp, ctypes.POINTER(_sz)]),
+    "iskv_exact_status": (_i, [_vp]),
 }
 
 
@@ -391,3 +392,7 @@ def iskv_prefix_decode_workspace(rows, q, prefix):
     n = _sz(0)
     code = lib.iskv_prefix_decode_workspace(_ref(rows), _ref(q), _ref(prefix), ctypes.byref(n))
     return code, n.value
+
+
+def iskv_exact_status(stream=None) -> int:
+    return lib.iskv_exact_status(_stream(stream))

@@ -18,6 +18,7 @@ constexpr int EX_D = 128;
 constexpr int EX_QROWS = 8;            // query rows of a split-kernel tile (tokens x GQA group)
 constexpr int EX_REC = EX_QROWS * (2 + EX_D);   // floats of a record: m[8], l[8], O[8][128]
 constexpr int EX_MAXREC = 1024;        // records that one merge block can combine
+constexpr int EX_PRE_MAX = 256;        // of them at most from the tile kernel
 
 struct ExactArgs {
     const char *k, *v;                 // rows of the sequences
@@ -46,6 +47,7 @@ struct ExactArgs {
     int direct;                        // 1: an item that one block covers writes its outputs itself
     float scale_log2;                  // log2(e) / sqrt(128)
     int grid;                          // blocks of the split kernel
+    int after;                         // 1: launched next to the kernel before it, whose end it awaits
 };
 
 // Tokens per tile of query rows.

@@ -7,6 +7,7 @@
 
 #include "evict.cuh"
 #include "exact.cuh"
+#include "exact_tile.cuh"
 #include "iskv_internal.cuh"
 
 using namespace iskv;
@@ -123,6 +124,142 @@ int launched(cudaError_t e) {
     return ISKV_ERR_CUDA;
 }
 
+// ---- the tile kernel: which calls take it, and how their work is cut ------------------------------
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+    static const EncodeTiledFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeTiledFn>(p);
+        cudaGetLastError();
+        return static_cast<EncodeTiledFn>(nullptr);
+    }();
+    return fn;
+}
+
+// 4-D map of bf16 vectors of 128 channels: extents and byte strides of the other dimensions, boxes
+// of 64 channels x box. Shared memory gets 128-byte rows, swizzled. False where the driver does not
+// take it (a stride of 0 over several items, say).
+bool encode_map(CUtensorMap *map, const void *base, const long long (&ext)[3],
+                const long long (&st)[3], const int (&box)[3]) {
+    const EncodeTiledFn enc = encode_tiled();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {EX_D, 0, 0, 0}, strides[3];
+    cuuint32_t boxes[4] = {64, 0, 0, 0}, steps[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 3; ++i) {
+        dims[i + 1] = (cuuint64_t)ext[i];
+        strides[i] = (cuuint64_t)(ext[i] > 1 ? st[i] : 256);
+        boxes[i + 1] = (cuuint32_t)box[i];
+        if (strides[i] == 0) return false;
+    }
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides,
+               boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct TilePlan {
+    bool use, alternate;
+    int tq, pairs, nsp, records;
+};
+
+// `tokens` query tokens (prefix: sequences) per unit, over at most `seen` rows each.
+TilePlan tile_plan(int units, int tokens, int G, long long seen, int sms) {
+    TilePlan p;
+    memset(&p, 0, sizeof(p));
+    // one tile of 8 query rows reads the rows once in the split kernel as well
+    p.use = tokens * (long long)G > EX_QROWS && seen > 0;
+    if (!p.use) return p;
+    p.tq = TILE_ROWS / G;
+    const long long tiles = (tokens + p.tq - 1) / p.tq;
+    p.alternate = tiles == 1;                 // one tile: the CTA's halves share out its blocks
+    p.pairs = (int)(p.alternate ? 1 : (tiles + 1) / 2);
+    const long long ctas = (long long)units * p.pairs;
+    const long long blocks = (seen + TILE_ROWS - 1) / TILE_ROWS;
+    // fewer CTAs than SMs: split the rows, in parts of four blocks at least
+    long long nsp = ctas >= sms ? 1 : sms / ctas;
+    const long long most = blocks / 4 > 1 ? blocks / 4 : 1;
+    if (nsp > most) nsp = most;
+    if (nsp > EX_PRE_MAX / 2) nsp = EX_PRE_MAX / 2;
+    p.nsp = (int)nsp;
+    p.records = p.nsp * (p.alternate ? 2 : 1);
+    return p;
+}
+size_t tile_record_bytes(const TilePlan &p, long long units, long long tokens, int G) {
+    if (!p.use) return 0;
+    return align256((size_t)(units * p.records * tokens * G) * 2 * sizeof(float)) +
+           align256((size_t)(units * p.records * tokens * G) * EX_D * sizeof(float));
+}
+
+bool all_bf16(const iskv_exact_rows *r, const iskv_exact_queries *q) {
+    return r->dtype == ISKV_BF16 && q->dtype == ISKV_BF16;
+}
+
+TilePlan window_plan(const iskv_exact_rows *r, const iskv_exact_queries *q, int window, int sinks,
+                     int sms) {
+    TilePlan none;
+    memset(&none, 0, sizeof(none));
+    if (!all_bf16(r, q)) return none;
+    const int G = q->n_q_heads / r->n_kv_heads;
+    // rows that a pair of tiles sees at most
+    const long long near = (long long)window + sinks + 2 * (TILE_ROWS / G);
+    return tile_plan(r->batch * r->n_kv_heads, q->m, G, near < r->rows ? near : r->rows, sms);
+}
+
+TilePlan prefix_plan(const iskv_exact_rows *r, const iskv_exact_queries *q,
+                     const iskv_exact_prefix *p, int sms) {
+    TilePlan none;
+    memset(&none, 0, sizeof(none));
+    if (!all_bf16(r, q)) return none;
+    return tile_plan(r->n_kv_heads, r->batch, q->n_q_heads / r->n_kv_heads, p->rows, sms);
+}
+
+// Fills the tile kernel's arguments and maps; false: the rows or queries cannot be mapped.
+bool tile_args(TileArgs &t, CUtensorMap *maps, const TilePlan &p, const ExactArgs &a, bool prefix,
+               float *records) {
+    memset(&t, 0, sizeof(t));
+    t.B = a.B;
+    t.H = a.H;
+    t.G = a.G;
+    t.rows = prefix ? a.P : a.rows;
+    t.lens = a.lens;
+    t.q_lens = a.q_lens;
+    t.m = prefix ? a.B : a.m;
+    t.window = a.window;
+    t.sinks = a.sinks;
+    t.tq = p.tq;
+    t.pairs = p.pairs;
+    t.nsp = p.nsp;
+    t.records = p.records;
+    t.out = a.out;
+    t.o_seq = a.o_seq;
+    t.o_head = a.o_head;
+    t.o_tok = a.o_tok;
+    t.scale_log2 = a.scale_log2;
+    t.pre_ml = records;
+    if (records)
+        t.pre_o = reinterpret_cast<float *>(
+            reinterpret_cast<char *>(records) +
+            align256((size_t)(prefix ? a.H : a.B * a.H) * p.records * t.m * a.G * 2 * sizeof(float)));
+    if (!encode_map(&maps[0], a.q, {(long long)a.H * a.G, a.m, a.B}, {a.q_head, a.q_tok, a.q_seq},
+                    {a.G, prefix ? 1 : p.tq, prefix ? p.tq : 1}))
+        return false;
+    const char *kv[2] = {prefix ? a.pk : a.k, prefix ? a.pv : a.v};
+    for (int i = 0; i < 2; ++i)
+        if (!encode_map(&maps[1 + i], kv[i], {t.rows, a.H, prefix ? 1 : a.B},
+                        {prefix ? a.p_row : a.row_st, prefix ? a.p_head : a.head_st, a.seq_st},
+                        {TILE_ROWS, 1, 1}))
+            return false;
+    return true;
+}
+
 int run_split(const ExactArgs &a, const iskv_exact_rows *r, const iskv_exact_queries *q,
               cudaStream_t s) {
     const bool fr = r->dtype == ISKV_F32, fi = q->dtype == ISKV_F32;
@@ -140,7 +277,13 @@ extern "C" int iskv_window_attn_workspace(const iskv_exact_rows *r, const iskv_e
     if (rc != ISKV_OK) return rc;
     const int sms = sm_count();
     if (!sms) return ISKV_ERR_CUDA;
-    *bytes = record_bytes(sms, 0);
+    const TilePlan p = window_plan(r, q, window, sinks, sms);
+    const size_t split = record_bytes(sms, 0);
+    const size_t tile =
+        p.records > 1 ? tile_record_bytes(p, (long long)r->batch * r->n_kv_heads, q->m,
+                                          q->n_q_heads / r->n_kv_heads)
+                      : 0;
+    *bytes = split > tile ? split : tile;
     return ISKV_OK;
 }
 
@@ -155,9 +298,21 @@ extern "C" int iskv_window_attn(const iskv_exact_rows *r, const iskv_exact_queri
     fill(a, r, q, sm_count());
     a.window = window < kMaxRows ? window : (int)kMaxRows;
     a.sinks = sinks < r->rows ? sinks : r->rows;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const TilePlan p = window_plan(r, q, window, sinks, a.grid);
+    if (p.use) {
+        TileArgs t;
+        CUtensorMap maps[3];
+        if (tile_args(t, maps, p, a, false, p.records > 1 ? static_cast<float *>(ws) : nullptr)) {
+            const int e = launched(
+                launch_exact_tile(t, maps[0], maps[1], maps[2], false, p.alternate, s));
+            if (e != ISKV_OK || p.records == 1) return e;
+            return launched(launch_exact_tile_merge(t, s));
+        }
+    }
     a.direct = 1;
     a.rec = static_cast<float *>(ws);
-    return run_split(a, r, q, reinterpret_cast<cudaStream_t>(stream));
+    return run_split(a, r, q, s);
 }
 
 extern "C" int iskv_mass_decode_workspace(const iskv_exact_rows *r, const iskv_exact_queries *q,
@@ -209,7 +364,9 @@ extern "C" int iskv_prefix_decode_workspace(const iskv_exact_rows *r, const iskv
     if (!sms) return ISKV_ERR_CUDA;
     const int tpt = ex_tpt(q->n_q_heads / r->n_kv_heads);
     const long long tiles = (r->batch + tpt - 1) / tpt;
-    *bytes = record_bytes(sms, (long long)r->n_kv_heads * (r->batch + tiles));
+    *bytes = record_bytes(sms, (long long)r->n_kv_heads * (r->batch + tiles)) +
+             tile_record_bytes(prefix_plan(r, q, p, sms), r->n_kv_heads, r->batch,
+                               q->n_q_heads / r->n_kv_heads);
     return ISKV_OK;
 }
 
@@ -230,8 +387,28 @@ extern "C" int iskv_prefix_decode(const iskv_exact_rows *r, const iskv_exact_que
     a.p_row = p->row_stride * e;
     a.P = p->rows;
     a.rec = static_cast<float *>(ws);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const TilePlan plan = prefix_plan(r, q, p, a.grid);
+    if (plan.use) {
+        const int tpt = ex_tpt(a.G);
+        const size_t at =
+            record_bytes(a.grid, (long long)a.H * (a.B + (a.B + tpt - 1) / tpt));
+        TileArgs t;
+        CUtensorMap maps[3];
+        if (tile_args(t, maps, plan, a, true,
+                      reinterpret_cast<float *>(static_cast<char *>(ws) + at))) {
+            const int e2 =
+                launched(launch_exact_tile(t, maps[0], maps[1], maps[2], true, plan.alternate, s));
+            if (e2 != ISKV_OK) return e2;
+            a.pre_ml = t.pre_ml;
+            a.pre_o = t.pre_o;
+            a.nsp = plan.records;
+            a.after = 1;
+            return run_split(a, r, q, s);
+        }
+    }
     a.shared_here = p->rows > 0;
-    return run_split(a, r, q, reinterpret_cast<cudaStream_t>(stream));
+    return run_split(a, r, q, s);
 }
 
 extern "C" int iskv_evict_workspace(const iskv_exact_rows *r, int budget, size_t *bytes) {
@@ -290,4 +467,11 @@ extern "C" int iskv_evict(const iskv_exact_rows *r, const float *mass, float *ma
     a.keep = a.n_moves + units;
     a.moves = reinterpret_cast<int *>(static_cast<char *>(ws) + align256((size_t)units * 8));
     return launched(launch_evict(a, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int iskv_exact_status(iskv_stream_t stream) {
+    int timed_out = 0;
+    const int rc =
+        launched(exact_tile_status(&timed_out, reinterpret_cast<cudaStream_t>(stream)));
+    return rc != ISKV_OK ? rc : timed_out ? ISKV_ERR_TIMEOUT : ISKV_OK;
 }

@@ -14,10 +14,16 @@
 // terms and both sums land in one thread; lo takes a second one. The same for the weights p, so
 // that float32 outputs keep float32 accuracy (a weight rounded to bf16 would cost 2^-9).
 //
+// Tensor cores truncate where they add, always toward zero: over the hundred steps of a long cache
+// the outputs lost 4e-6. So each step's products start from zero and are added to the outputs in
+// float32 arithmetic (round to nearest), smallest terms first: 8e-7 at 8 x 32768 rows.
+//
 // The flat space of (item, step) is cut into equal ranges, one per block, so that sequences of any
 // lengths fill the GPU evenly. An item that several blocks share leaves one record per block,
 // which the merge kernel joins: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
 #include <math_constants.h>
+
+#include <atomic>
 
 #include "exact.cuh"
 
@@ -220,7 +226,10 @@ __global__ void __launch_bounds__(32 * ex_warps(F32ROWS), 1) exact_split_kernel(
     const long long total = ex_total(a, RS);
     const long long per = (total + a.grid - 1) / a.grid;
     const long long g0 = blockIdx.x * per, g1 = min(total, g0 + per);
-    if (g0 >= g1) return;
+    if (g0 >= g1) {
+        if (a.after) asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
 
     Item it = find_item<RS>(a, g0), nx = it;
     long long at = g0, ahead = g0;                   // flat steps: computed, loaded
@@ -261,7 +270,7 @@ __global__ void __launch_bounds__(32 * ex_warps(F32ROWS), 1) exact_split_kernel(
     bool fresh = true;                               // a new item begins: its queries are read
     long long seg0 = at;
     uint32_t qh[8][2], qm[F32IO ? 8 : 1][2], ql[F32IO ? 8 : 1][2];
-    float o[16][4];
+    float o[16][2];
     float m = -CUDART_INF_F, l = 0.f;
     int pos = 0;                                     // position of this lane's query row
     const int tok = g / a.G, head = g - tok * a.G;
@@ -291,7 +300,7 @@ __global__ void __launch_bounds__(32 * ex_warps(F32ROWS), 1) exact_split_kernel(
                     }
                 }
 #pragma unroll
-            for (int i2 = 0; i2 < 16; ++i2) o[i2][0] = o[i2][1] = o[i2][2] = o[i2][3] = 0.f;
+            for (int i2 = 0; i2 < 16; ++i2) o[i2][0] = o[i2][1] = 0.f;
             m = -CUDART_INF_F;
             l = 0.f;
         }
@@ -373,7 +382,7 @@ __global__ void __launch_bounds__(32 * ex_warps(F32ROWS), 1) exact_split_kernel(
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) o[i][x] *= f;
+                    for (int x = 0; x < 2; ++x) o[i][x] *= f;
             }
             const float ref = m == -CUDART_INF_F ? 0.f : m;
 #pragma unroll
@@ -394,9 +403,12 @@ __global__ void __launch_bounds__(32 * ex_warps(F32ROWS), 1) exact_split_kernel(
                     ldsm4t(smem_addr(vs_ + r * RB + (((2 * i + cc) ^ (r & 7)) * 16)), vb);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        mma(o[2 * i + x], ph[0], pm[0], ph[1], pm[1], vb[2 * x], vb[2 * x + 1]);
+                        float c[4] = {0.f, 0.f, 0.f, 0.f};
                         if constexpr (F32IO)
-                            mma(o[2 * i + x], pl[0], 0u, pl[1], 0u, vb[2 * x], vb[2 * x + 1]);
+                            mma(c, pl[0], 0u, pl[1], 0u, vb[2 * x], vb[2 * x + 1]);
+                        mma(c, ph[0], pm[0], ph[1], pm[1], vb[2 * x], vb[2 * x + 1]);
+                        o[2 * i + x][0] += c[0] + c[2];
+                        o[2 * i + x][1] += c[1] + c[3];
                     }
                 }
             } else {
@@ -416,10 +428,13 @@ __global__ void __launch_bounds__(32 * ex_warps(F32ROWS), 1) exact_split_kernel(
                         }
                         split3(f[0], f[1], vh[x], vm[x], vl[x]);
                     }
-                    mma(o[i], ph[0], pm[0], ph[1], pm[1], vh[0], vh[1]);
-                    mma(o[i], ph[0], pm[0], ph[1], pm[1], vm[0], vm[1]);
-                    mma(o[i], ph[0], pm[0], ph[1], pm[1], vl[0], vl[1]);
-                    mma(o[i], pl[0], 0u, pl[1], 0u, vh[0], vh[1]);
+                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma(c, ph[0], pm[0], ph[1], pm[1], vl[0], vl[1]);
+                    mma(c, pl[0], 0u, pl[1], 0u, vh[0], vh[1]);
+                    mma(c, ph[0], pm[0], ph[1], pm[1], vm[0], vm[1]);
+                    mma(c, ph[0], pm[0], ph[1], pm[1], vh[0], vh[1]);
+                    o[i][0] += c[0] + c[2];
+                    o[i][1] += c[1] + c[3];
                 }
             }
         }
@@ -435,8 +450,7 @@ __global__ void __launch_bounds__(32 * ex_warps(F32ROWS), 1) exact_split_kernel(
         float *mine = red + (warp * EX_QROWS + g) * EX_D + 2 * t;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            *reinterpret_cast<float2 *>(mine + 8 * i) =
-                make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3]);
+            *reinterpret_cast<float2 *>(mine + 8 * i) = make_float2(o[i][0], o[i][1]);
         if (t == 0) {
             red_m[warp * EX_QROWS + g] = m;
             red_l[warp * EX_QROWS + g] = l;
@@ -491,6 +505,8 @@ __global__ void __launch_bounds__(32 * ex_warps(F32ROWS), 1) exact_split_kernel(
         if (at < g1) next_item<RS>(a, it);
     }
     cp_wait<0>();
+    // the merge waits for this kernel alone: it must not end before the one that ran beside it
+    if (a.after) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---- merge --------------------------------------------------------------------------------------
@@ -663,6 +679,18 @@ __global__ void __launch_bounds__(MERGE_T) exact_merge_kernel(ExactArgs a, int r
     }
 }
 
+// The kernel's shared-memory limit, set on the first launch on each device.
+cudaError_t once_per_device(std::atomic<unsigned long long> &set, const void *kern, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (set.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) set.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 template <bool F32ROWS>
 constexpr size_t split_smem() {
     constexpr int W = ex_warps(F32ROWS);
@@ -673,10 +701,20 @@ template <bool F32ROWS, bool F32IO, bool MASS>
 cudaError_t split(const ExactArgs &a, cudaStream_t s) {
     auto kern = exact_split_kernel<F32ROWS, F32IO, MASS>;
     const size_t bytes = split_smem<F32ROWS>();
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    static std::atomic<unsigned long long> set{0};   // devices whose attribute is set
+    const cudaError_t e = once_per_device(set, reinterpret_cast<const void *>(kern), (int)bytes);
     if (e != cudaSuccess) return e;
-    kern<<<a.grid, 32 * ex_warps(F32ROWS), bytes, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.grid);
+    cfg.blockDim = dim3(32 * ex_warps(F32ROWS));
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = a.after ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <bool F32ROWS, bool F32IO, bool MASS>

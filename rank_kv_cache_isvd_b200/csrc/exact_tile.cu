@@ -1,0 +1,656 @@
+// Attention of many query rows over exact rows on the tensor cores (tcgen05), for prompts, chunks of
+// them, and a prefix that a batch shares.
+//
+//   S = Q K^T (128 query rows x 128 key rows),  P = 2^(S c - m),  O = O 2^(m_old - m) + P V
+//
+// with c = log2(e)/sqrt(128), one pass over the key blocks, m and the sum l of P per query row in
+// registers. A tile's 128 query rows are tokens x the q-heads of one kv-head, so that the group
+// shares every key block, and a window covers few blocks: 32 tokens per tile at a group of 4.
+//
+// One CTA of 384 threads per SM works on two tiles at once:
+// - warp 0 loads Q once and then K and V blocks by TMA into a ring of five 32 KB stages;
+// - warp 1 issues the products. S of tile i sits in tensor memory columns 128 i .. , its P (bf16)
+//   overwrites the first half of them and is the A operand of P V; O sits in columns 256 + 128 i;
+// - warps 4-7 and 8-11 are the softmax of tile 0 and of tile 1: a thread owns a query row, so
+//   maxima and sums need no shuffles. While one group computes, the tensor cores work for the other.
+//
+// m moves only when a row's maximum passes it by 2^8 (a power of two that P, O and l carry along
+// exactly enough: P is at most 256). Moving it rescales O in tensor memory, which the softmax warp
+// does itself: S of this block being complete says that the P V before it is too.
+//
+// P is rounded to bf16 (half a step, 2^-9 of the leading bits' scale, at random over the keys);
+// the sum l takes the unrounded values, and all sums are float32.
+//
+// Every wait is bounded. A wait that gives up sets the CTA's abort flag and the device's status
+// word; all roles then leave their loops, copies in flight are waited for, and tensor memory is
+// freed.
+#include <math_constants.h>
+
+#include <atomic>
+
+#include "exact.cuh"
+#include "exact_tile.cuh"
+#include "tc_util.cuh"
+
+namespace iskv {
+namespace {
+
+constexpr int TT = 384;
+constexpr int NSTAGE = 5;
+constexpr int BLOCK_BYTES = 128 * 256;       // 128 rows of 128 bf16: two halves of 64 channels
+constexpr int HALF_BYTES = 128 * 128;
+constexpr uint32_t POLLS = 1u << 18, SUSPEND_NS = 20000;
+
+// setmaxnreg: 128 control threads and 256 softmax threads share what the launch was given
+constexpr int REG_LO = 72, REG_HI = 216, REG_LAUNCH = 168;
+static_assert(128 * REG_LO + 256 * REG_HI <= TT * REG_LAUNCH, "register split");
+
+__device__ int g_tile_status;
+
+struct Bars {
+    uint64_t q_full, kv_full[NSTAGE], kv_empty[NSTAGE], s_full[2], p_full[2], o_full[2];
+    uint32_t tmem;
+    int abort, issued;
+};
+constexpr size_t TILE_SMEM = 2 * BLOCK_BYTES + NSTAGE * BLOCK_BYTES + sizeof(Bars) + 1024;
+
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    const uint32_t a = smem_u32(bar);
+    for (uint32_t i = 0; i < POLLS; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(a), "r"(parity), "r"(SUSPEND_NS)
+            : "memory");
+        if (done) return true;
+        if (*abort) return false;
+    }
+    *abort = 1;
+    return false;
+}
+__device__ __forceinline__ void arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                            int w, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+// D[tmem] (+)= A[smem] B[smem]^T and D[tmem] (+)= A[tmem] B[smem]^T, bf16 operands.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// Descriptor of an operand whose M or N index is contiguous (V: channels), 128-byte swizzle: 64
+// channels x 8 rows per 1024 bytes, the next 8 rows 1024 bytes on, the next 64 channels one half on.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(HALF_BYTES >> 4) << 16 |
+           (uint64_t)(1024u >> 4) << 32 | (uint64_t)1u << 46 | (uint64_t)2u << 61;
+}
+// D fp32, A and B bf16, 128 x 128; b_mn: B's N index is contiguous.
+__host__ __device__ constexpr uint32_t idesc_tile(bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((128u >> 3) << 17) |
+           ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+        "%10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+        "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+        "r"(r[30]), "r"(r[31]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack(float x, float y) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// (a0, a1) * b + (c, c) in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// What a CTA works on. PREFIX: "tokens" are the batch's sequences, the rows have no sequence, and
+// every row is visible.
+struct Work {
+    int b, h, t0;              // sequence, kv-head, first token of the pair of tiles
+    int sp;                    // split
+    int n, ql;
+    int p0, p1;                // lowest and highest position of the pair's tokens
+    int nsb, wb0;              // blocks 0 .. nsb - 1 hold sinks, then blocks from wb0 on
+    int first, count;          // this CTA's blocks: first .. first + count - 1 of those
+    __device__ int base(int i) const {
+        const int x = first + i;
+        return (x < nsb ? x : wb0 + x - nsb) * TILE_ROWS;
+    }
+};
+
+template <bool PREFIX>
+__device__ __forceinline__ Work work_of(const TileArgs &a, bool alternate) {
+    Work w;
+    // pairs in descending order, kv-heads and sequences within: the longest rows start first
+    int id = blockIdx.x;
+    const int bh = PREFIX ? a.H : a.B * a.H;
+    const int unit = id % bh;
+    id /= bh;
+    w.sp = id % a.nsp;
+    const int pair = a.pairs - 1 - id / a.nsp;
+    w.b = PREFIX ? 0 : unit / a.H;
+    w.h = PREFIX ? unit : unit - w.b * a.H;
+    w.t0 = pair * (alternate ? 1 : 2) * a.tq;
+    if (PREFIX) {
+        w.n = a.rows;
+        w.ql = a.m;
+        w.p0 = w.p1 = a.rows - 1;
+        w.nsb = 0;
+        w.wb0 = 0;
+        w.count = (a.rows + TILE_ROWS - 1) / TILE_ROWS;
+    } else {
+        w.n = min(max(a.lens ? a.lens[w.b] : a.rows, 0), a.rows);
+        w.ql = min(max(a.q_lens ? a.q_lens[w.b] : a.m, 0), a.m);
+        const int t1 = min(w.t0 + (alternate ? 1 : 2) * a.tq, w.ql);
+        w.p0 = w.n - w.ql + w.t0;
+        w.p1 = w.n - w.ql + t1 - 1;
+        const int hi = max(0, w.p1 + 1), sk = min(a.sinks, hi);
+        const int lo = max(0, w.p0 - a.window + 1);
+        w.wb0 = min(lo, hi) / TILE_ROWS;
+        const int end = (hi + TILE_ROWS - 1) / TILE_ROWS;
+        w.nsb = min((sk + TILE_ROWS - 1) / TILE_ROWS, w.wb0);
+        w.count = w.nsb + max(0, end - w.wb0);
+    }
+    const long long all = w.count;
+    w.first = (int)(all * w.sp / a.nsp);
+    w.count = (int)(all * (w.sp + 1) / a.nsp) - w.first;
+    return w;
+}
+
+template <bool PREFIX, bool ALT>
+__global__ void __launch_bounds__(TT, 1)
+exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CUtensorMap qmap,
+                  const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap) {
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    uint8_t *qs = smem, *ring = smem + 2 * BLOCK_BYTES;
+    Bars *bars = reinterpret_cast<Bars *>(ring + NSTAGE * BLOCK_BYTES);
+    volatile int *abort_flag = &bars->abort;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Work w = work_of<PREFIX>(a, ALT);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (w.t0 >= w.ql) return;
+    const int N = w.count;
+
+    if (tid == 0) {
+        mbar_init(&bars->q_full, 1);
+        for (int i = 0; i < NSTAGE; ++i) {
+            mbar_init(&bars->kv_full[i], 1);
+            mbar_init(&bars->kv_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->s_full[i], 1);
+            mbar_init(&bars->p_full[i], 4);
+            mbar_init(&bars->o_full[i], 1);
+        }
+        bars->abort = bars->issued = 0;
+        fence_mbar_init();
+    }
+    if (warp == 2) tmem_alloc(&bars->tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+
+    // The order in which blocks' keys and values enter the ring is the order in which the products
+    // take them: both tiles on every block: K0 V0 K1 V1 ...; the two groups on alternate blocks of
+    // one tile: K0 K1 V0 K2 V1 K3 ...
+    constexpr int AHEAD = ALT ? 2 : 1;
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LO));
+      if (warp == 0) {
+        if (lane == 0 && N > 0) {
+            constexpr int QT = ALT ? 1 : 2;
+            const uint32_t q_bytes = (uint32_t)QT * a.tq * a.G * 256;
+            mbar_arrive_expect_tx(&bars->q_full, q_bytes);
+            for (int i = 0; i < QT; ++i)
+                for (int x = 0; x < 2; ++x) {
+                    uint8_t *dst = qs + i * BLOCK_BYTES + x * HALF_BYTES;
+                    const int t = w.t0 + i * a.tq;
+                    if (PREFIX) tma_load_4d(dst, &qmap, x * 64, w.h * a.G, 0, t, &bars->q_full);
+                    else tma_load_4d(dst, &qmap, x * 64, w.h * a.G, t, w.b, &bars->q_full);
+                }
+            int issued = 0;
+            auto load = [&](const CUtensorMap *map, int blk) {
+                const int st = issued % NSTAGE;
+                if (issued >= NSTAGE &&
+                    !wait_bar(&bars->kv_empty[st], (issued / NSTAGE + 1) & 1, abort_flag))
+                    return false;
+                const int row = w.base(blk);
+                mbar_arrive_expect_tx(&bars->kv_full[st], BLOCK_BYTES);
+                for (int x = 0; x < 2; ++x)
+                    tma_load_4d(ring + st * BLOCK_BYTES + x * HALF_BYTES, map, x * 64, row, w.h, w.b,
+                                &bars->kv_full[st]);
+                ++issued;
+                return true;
+            };
+            bool ok = true;
+            for (int j = 0; ok && j < AHEAD && j < N; ++j) ok = load(&kmap, j);
+            for (int j = 0; ok && j < N; ++j) {
+                ok = load(&vmap, j);
+                if (ok && j + AHEAD < N) ok = load(&kmap, j + AHEAD);
+            }
+            bars->issued = issued;
+        }
+      } else if (warp == 1) {
+        int use = 0;                                   // blocks taken from the ring
+        auto wait = [&](uint64_t *bar, uint32_t parity) {   // the same answer in every lane
+            return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag)) != 0;
+        };
+        auto full = [&]() {
+            return wait(&bars->kv_full[use % NSTAGE], (use / NSTAGE) & 1);
+        };
+        auto stage_addr = [&]() { return smem_u32(ring + (use % NSTAGE) * BLOCK_BYTES); };
+        auto qk = [&](int i) {                          // S_i = Q_i K^T
+            const uint32_t q = smem_u32(qs + (ALT ? 0 : i) * BLOCK_BYTES), k = stage_addr();
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const uint32_t off = (s >> 2) * HALF_BYTES + (s & 3) * 32;
+                mma_ss(tmem + i * 128, sw128_kmajor_desc(q + off), sw128_kmajor_desc(k + off),
+                       idesc_tile(false), s > 0);
+            }
+            mma_commit(&bars->s_full[i]);
+        };
+        auto pv = [&](int i, bool acc) {                // O_i (+)= P_i V
+            const uint32_t v = stage_addr();
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                mma_ts(tmem + 256 + i * 128, tmem + i * 128 + s * 8, sw128_mnmajor_desc(v + s * 2048),
+                       idesc_tile(true), acc || s > 0);
+        };
+        // Values of rows that no token of the pair sees may be anything: 0 x NaN would reach O.
+        auto scrub = [&](int blk) {
+            if (PREFIX) return;
+            const int base = w.base(blk);
+            const bool tail = base + TILE_ROWS - 1 > w.p1;
+            const bool gap = base <= w.p0 - a.window && base + TILE_ROWS > a.sinks;
+            if (!tail && !gap) return;
+            uint8_t *v = ring + (use % NSTAGE) * BLOCK_BYTES;
+            for (int r = lane; r < TILE_ROWS; r += 32) {
+                const int j = base + r;
+                if (j <= w.p1 && (j < a.sinks || j > w.p0 - a.window)) continue;
+                for (int x = 0; x < 16; ++x)
+                    *reinterpret_cast<uint4 *>(v + (x >> 3) * HALF_BYTES + r * 128 + (x & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
+        auto release = [&]() {
+            if (lane == 0) mma_commit(&bars->kv_empty[use % NSTAGE]);
+            ++use;
+        };
+        bool ok = N > 0 && wait(&bars->q_full, 0);
+        if (!ALT) {
+            if (ok) ok = full();
+            if (ok) {
+                if (lane == 0) {
+                    qk(0);
+                    qk(1);
+                }
+                release();
+            }
+            for (int j = 0; ok && j < N; ++j) {
+                ok = full();                            // V_j
+                if (ok) scrub(j);
+                if (ok) ok = wait(&bars->p_full[0], j & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) pv(0, j > 0);
+                const int v_use = use;
+                if (j + 1 < N) {
+                    ++use;
+                    ok = full();                        // K_j+1
+                    if (!ok) break;
+                    if (lane == 0) qk(0);
+                    use = v_use;
+                }
+                ok = wait(&bars->p_full[1], j & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) pv(1, j > 0);
+                release();
+                if (j + 1 < N) {
+                    if (lane == 0) qk(1);
+                    release();
+                }
+            }
+        } else {
+            for (int i = 0; ok && i < 2 && i < N; ++i) {
+                ok = full();
+                if (!ok) break;
+                if (lane == 0) qk(i);
+                release();
+            }
+            for (int j = 0; ok && j < N; ++j) {
+                const int i = j & 1;
+                ok = full();
+                if (ok) scrub(j);
+                if (ok) ok = wait(&bars->p_full[i], (j >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) pv(i, j > 1);
+                release();
+                if (j + 2 < N) {
+                    ok = full();
+                    if (!ok) break;
+                    if (lane == 0) qk(i);
+                    release();
+                }
+            }
+        }
+        // commits follow all products before them, so these come when both tiles are complete;
+        // after an abort they bound what is in flight
+        if (lane == 0 && N > 0) {
+            mma_commit(&bars->o_full[0]);
+            mma_commit(&bars->o_full[1]);
+        }
+      }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_HI));
+        const int i = (warp - 4) >> 2;                  // tile (ALT: share of the blocks)
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lane_bits = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_t = tmem + i * 128 + lane_bits, o_t = tmem + 256 + i * 128 + lane_bits;
+        const int tl = row / a.G, gq = row - tl * a.G;
+        const int tok = w.t0 + (ALT ? 0 : i * a.tq) + tl;
+        const bool live = tl < a.tq && tok < w.ql;
+        const int pos = PREFIX ? w.n - 1 : w.n - w.ql + tok;
+        // the tile's own range of positions: blocks inside every token's view need no mask
+        const int tile0 = w.t0 + (ALT ? 0 : i * a.tq);
+        const int tp0 = PREFIX ? w.n - 1 : w.n - w.ql + tile0;
+        const int tp1 = PREFIX ? w.n - 1 : w.n - w.ql + min(tile0 + a.tq, w.ql) - 1;
+        const int mine = ALT ? (N - i + 1) / 2 : N;
+        float m = -CUDART_INF_F;
+        float2 l2 = make_float2(0.f, 0.f);
+        bool ok = true;
+        for (int x = 0; x < mine; ++x) {
+            ok = wait_bar(&bars->s_full[i], x & 1, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            float s[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(s_t + c * 32, s[c]);
+            tmem_wait_ld();
+            const int base = w.base(ALT ? 2 * x + i : x);
+            const bool inside = PREFIX ? base + TILE_ROWS <= w.n
+                                       : base + TILE_ROWS - 1 <= tp0 &&
+                                             (base + TILE_ROWS <= a.sinks || base > tp1 - a.window);
+            if (!inside) {
+                const int hi = pos - base, lo = PREFIX ? 0 : pos - a.window + 1 - base;
+                const int sk = PREFIX ? 0 : a.sinks - base;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int j = c * 32 + e;
+                        if (!(j <= hi && (j >= lo || j < sk))) s[c][e] = -CUDART_INF_F;
+                    }
+            }
+            float t0 = s[0][0], t1 = s[1][0], t2 = s[2][0], t3 = s[3][0];
+#pragma unroll
+            for (int e = 1; e < 32; ++e) {
+                t0 = fmaxf(t0, s[0][e]);
+                t1 = fmaxf(t1, s[1][e]);
+                t2 = fmaxf(t2, s[2][e]);
+                t3 = fmaxf(t3, s[3][e]);
+            }
+            const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * a.scale_log2;
+            const bool raise = top > m + 8.f || (m == -CUDART_INF_F && top > m);
+            if (__any_sync(0xffffffffu, raise)) {
+                const float nm = raise ? top : m;
+                const float f = m == -CUDART_INF_F ? 0.f : ex2(m - nm);
+                m = nm;
+                l2.x *= f;
+                l2.y *= f;
+                if (x > 0) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float o[32];
+                        uint32_t u[32];
+                        tmem_ld32(o_t + c * 32, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
+                        tmem_st32(o_t + c * 32, u);
+                    }
+                }
+            }
+            const float ref = m == -CUDART_INF_F ? 0.f : m;
+            const float2 sc = make_float2(a.scale_log2, a.scale_log2), nr = make_float2(-ref, -ref);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t p[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const int q = c * 64 + 2 * e;
+                    float2 y = fma2(make_float2(s[q >> 5][q & 31], s[q >> 5][(q & 31) + 1]), sc, nr);
+                    y.x = ex2(y.x);
+                    y.y = ex2(y.y);
+                    l2 = add2(l2, y);
+                    p[e] = pack(y.x, y.y);
+                }
+                tmem_st32(s_t + c * 32, p);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(&bars->p_full[i]);
+        }
+        // ---- the tile is complete: out = O / l, or a record of this split -----------------------
+        const float l = l2.x + l2.y;
+        if (N > 0 && ok) {
+            ok = wait_bar(&bars->o_full[i], 0, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+        }
+        if (ok) {
+            const bool record = PREFIX || a.records > 1;
+            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+            char *op = nullptr;
+            float *ro = nullptr;
+            if (record) {
+                const int rec = ALT ? 2 * w.sp + i : w.sp;
+                const long long at =
+                    ((long long)(w.b * a.H + w.h) * a.records + rec) * a.m * a.G +
+                    (long long)tok * a.G + gq;
+                ro = a.pre_o + at * EX_D;
+                if (live) {
+                    a.pre_ml[2 * at] = m;
+                    a.pre_ml[2 * at + 1] = l;
+                }
+            } else {
+                op = a.out + w.b * a.o_seq + (long long)(w.h * a.G + gq) * a.o_head + tok * a.o_tok;
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float o[32];
+                if (mine > 0) {
+                    tmem_ld32(o_t + c * 32, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                }
+                if (!live) continue;
+                if (record) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4 *>(ro + c * 32 + e) =
+                            make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4 *>(op + (c * 32 + e) * 2) = make_uint4(
+                            pack(o[e] * inv, o[e + 1] * inv), pack(o[e + 2] * inv, o[e + 3] * inv),
+                            pack(o[e + 4] * inv, o[e + 5] * inv), pack(o[e + 6] * inv, o[e + 7] * inv));
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (tid == 0 && *abort_flag) {
+        // products and copies in flight end before the block does (bounded waits)
+        atomicExch(&g_tile_status, 1);
+        if (N > 0) {
+            bool late = !mbar_wait(&bars->o_full[1], 0) | !mbar_wait(&bars->q_full, 0);
+            for (int i = max(0, bars->issued - NSTAGE); i < bars->issued; ++i)
+                late |= !mbar_wait(&bars->kv_full[i % NSTAGE], (i / NSTAGE) & 1);
+            (void)late;
+        }
+    }
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the records of split rows: a warp per query row, four channels per lane.
+__global__ void __launch_bounds__(256) exact_tile_merge_kernel(const __grid_constant__ TileArgs a) {
+    const int lane = threadIdx.x & 31;
+    const long long per_unit = (long long)a.m * a.G;
+    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (row >= per_unit * a.B * a.H) return;
+    const int unit = (int)(row / per_unit), b = unit / a.H, h = unit - b * a.H;
+    const long long x = row - unit * per_unit;
+    const int tok = (int)(x / a.G), g = (int)(x - (long long)tok * a.G);
+    if (tok >= min(max(a.q_lens ? a.q_lens[b] : a.m, 0), a.m)) return;
+    const long long at = unit * per_unit * a.records + x;
+    float M = -CUDART_INF_F;
+    for (int r = 0; r < a.records; ++r) M = fmaxf(M, a.pre_ml[2 * (at + r * per_unit)]);
+    const float ref = M == -CUDART_INF_F ? 0.f : M;
+    float L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int r = 0; r < a.records; ++r) {
+        const float2 ml = *reinterpret_cast<const float2 *>(a.pre_ml + 2 * (at + r * per_unit));
+        const float f = ex2(ml.x - ref);
+        const float4 v =
+            *reinterpret_cast<const float4 *>(a.pre_o + (at + r * per_unit) * EX_D + lane * 4);
+        L += f * ml.y;
+        o.x += f * v.x;
+        o.y += f * v.y;
+        o.z += f * v.z;
+        o.w += f * v.w;
+    }
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+    char *op = a.out + b * a.o_seq + (long long)(h * a.G + g) * a.o_head + tok * a.o_tok;
+    *reinterpret_cast<uint2 *>(op + lane * 8) =
+        make_uint2(pack(o.x * inv, o.y * inv), pack(o.z * inv, o.w * inv));
+}
+
+template <bool PREFIX, bool ALT>
+cudaError_t launch(const TileArgs &a, const CUtensorMap &q, const CUtensorMap &k,
+                   const CUtensorMap &v, cudaStream_t s) {
+    auto kern = exact_tile_kernel<PREFIX, ALT>;
+    static std::atomic<unsigned long long> set{0};   // devices where the kernel may be launched
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(set.load(std::memory_order_acquire) & bit)) {
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, kern);
+        if (e != cudaSuccess) return e;
+        // setmaxnreg.inc draws on what the launch was given: less would wait for good
+        if (((fa.numRegs + 7) & ~7) < REG_LAUNCH) return cudaErrorLaunchOutOfResources;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TILE_SMEM);
+        if (e != cudaSuccess) return e;
+        set.fetch_or(bit, std::memory_order_release);
+    }
+    const long long blocks = (long long)(PREFIX ? a.H : a.B * a.H) * a.pairs * a.nsp;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    kern<<<(unsigned)blocks, TT, TILE_SMEM, s>>>(a, q, k, v);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_exact_tile(const TileArgs &a, const CUtensorMap &q, const CUtensorMap &k,
+                              const CUtensorMap &v, bool prefix, bool alternate, cudaStream_t s) {
+    if (prefix)
+        return alternate ? launch<true, true>(a, q, k, v, s) : launch<true, false>(a, q, k, v, s);
+    return alternate ? launch<false, true>(a, q, k, v, s) : launch<false, false>(a, q, k, v, s);
+}
+
+cudaError_t launch_exact_tile_merge(const TileArgs &a, cudaStream_t s) {
+    const long long blocks = ((long long)a.B * a.H * a.m * a.G + 7) / 8;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, exact_tile_merge_kernel, a);
+}
+
+cudaError_t exact_tile_status(int *timed_out, cudaStream_t s) {
+    int x = 0;
+    const int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&x, g_tile_status, sizeof(int), 0,
+                                              cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && x)
+        e = cudaMemcpyToSymbolAsync(g_tile_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    *timed_out = x;
+    return e;
+}
+
+}  // namespace iskv

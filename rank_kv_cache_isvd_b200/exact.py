@@ -8,8 +8,9 @@ import ctypes
 import torch
 
 from .binding import (ISKV_BF16, ISKV_F32, check, iskv_evict_workspace, iskv_exact_prefix,
-                      iskv_exact_queries, iskv_exact_rows, iskv_mass_decode_workspace,
-                      iskv_prefix_decode_workspace, iskv_window_attn_workspace, lib)
+                      iskv_exact_queries, iskv_exact_rows, iskv_exact_status,
+                      iskv_mass_decode_workspace, iskv_prefix_decode_workspace,
+                      iskv_window_attn_workspace, lib)
 
 D = 128
 _TYPES = {torch.bfloat16: ISKV_BF16, torch.float32: ISKV_F32}
@@ -142,7 +143,7 @@ class ExactKVCache:
         the rows ``j <= p`` with ``j < sinks`` or ``j > p - window``. A token that sees nothing gets
         zeros; outputs of tokens ``i >= q_lens[b]`` are not written."""
         (x, at), out, made, form = self._form(q, out, q_lens, True)
-        need = self._bytes(("iskv_window_attn", form),
+        need = self._bytes(("iskv_window_attn", form, window, sinks),
                            lambda: iskv_window_attn_workspace(self._rows, x, window, sinks))
         ws = self._workspace(need)
         s = self._stream(stream, ws, *([out] if made else []))
@@ -224,3 +225,9 @@ class ExactKVCache:
         s = self._stream(stream, ws, *([out] if made else []))
         self._call("iskv_prefix_decode", s, self._rows_at, at, p_at, ws.data_ptr(), need)
         return out
+
+    def status(self, stream=None) -> int:
+        """Status of the calls on exact caches on this device (synchronises): 0, or the code of a
+        device-side wait that gave up."""
+        with torch.cuda.device(self.device):
+            return iskv_exact_status(stream)
