@@ -341,8 +341,9 @@ int iskv_decode_attn_noalloc(const iskv_decode_view *view, const float *q_dev, f
  * q-head g reads kv-head g / (n_q/n_kv), and a query that sees no row gives zeros. Rows that no
  * query of their sequence sees are not used: they may hold anything, NaN included. Device arrays
  * of lengths are read on the device: values below 0 count as 0, values above the capacity as the
- * capacity. Strides count elements, have to be multiples of 16 bytes and may be 0 where rows or
- * queries are shared (never in outputs); a stride over an extent of 1 is not read.
+ * capacity. Strides count elements and have to be multiples of 16 bytes; those of sequences, heads
+ * and query tokens may be 0 where they share one place (never in outputs); a stride over an extent
+ * of 1 is not read.
  */
 typedef struct {
     const void *k, *v;       /* element (b, h, j, c) at b seq + h head + j row + c; 16-byte aligned */

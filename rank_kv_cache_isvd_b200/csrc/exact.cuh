@@ -6,6 +6,7 @@
 // j > p - window. With a shared prefix every token also sees all P prefix rows.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -21,8 +22,6 @@ constexpr int EX_MAXREC = 1024;        // records that one merge block can combi
 constexpr int EX_PRE_MAX = 256;        // of them at most from the tile kernel
 
 struct ExactArgs {
-    const char *k, *v;                 // rows of the sequences
-    long long seq_st, head_st, row_st; // bytes
     int B, H, rows;
     const int *lens;                   // NULL: every sequence holds `rows` rows
     const char *q;
@@ -32,10 +31,9 @@ struct ExactArgs {
     int G, m;
     const int *q_lens;                 // NULL: m tokens each
     int window, sinks;
-    const char *pk, *pv;               // shared prefix
-    long long p_head, p_row;           // bytes
-    int P;
+    int P;                             // shared prefix rows
     int shared_here;                   // 1: the split kernel computes the shared prefix too
+    int seq_mul, head_mul, p_head_mul; // 0 where all sequences, or kv-heads, share one stream
     float *rec;                        // records of the split kernel
     float *scores;                     // mass: scaled scores [B][H][G][score_st], log2 units
     long long score_st;
@@ -44,10 +42,16 @@ struct ExactArgs {
     const float *pre_ml;               // prefix records of the tile kernel: (m, l) [H][nsp][B*G][2]
     const float *pre_o;                //                                   O [H][nsp][B*G][128]
     int nsp;                           // their number of splits (0: none)
-    int direct;                        // 1: an item that one block covers writes its outputs itself
     float scale_log2;                  // log2(e) / sqrt(128)
     int grid;                          // blocks of the split kernel
+    int cluster;                       // by items: blocks per cluster, which share an item's steps
+    int by_items;                      // 1: a cluster takes whole items; 0: a block takes steps
     int after;                         // 1: launched next to the kernel before it, whose end it awaits
+};
+
+// Maps of the rows (see exact_api.cu): own keys and values, prefix keys and values.
+struct ExactMaps {
+    CUtensorMap k, v, pk, pv;
 };
 
 // Tokens per tile of query rows.
@@ -62,76 +66,74 @@ __device__ __forceinline__ int ex_qlen(const ExactArgs &a, int b) {
     return min(max(n, 0), a.m);
 }
 
-// The flat space of steps. Items in order: the shared prefix's (kv-head, tile of 8 (sequence,
-// q-head) rows), then every sequence's (kv-head, tile of 8 (token, q-head) rows). An item takes
-// S steps of `rs` rows; each block of the split kernel takes `per` consecutive steps.
+// Items in order: the shared prefix's (kv-head, tile of 8 (sequence, q-head) rows), then every
+// sequence's (kv-head, tile of 8 (token, q-head) rows). An item takes S steps of `rs` rows.
+// By steps: the flat space of (item, step) is cut into equal ranges, one per block. By items: the
+// list of items is, one range per cluster, whose blocks share out each item's steps.
 struct ExactSpan {
     int S;            // steps per item
     int RT;           // tiles per kv-head
+    int weight;       // length of an item in the space that is cut: S, or 1
 };
+
+// Rows that a tile of tpt tokens visits at most: its window, and the sinks in groups of 16.
+__host__ __device__ inline int ex_most_rows(int window, int sinks, int tpt, int n) {
+    const long long most = (long long)((sinks + 15) & ~15) + window + tpt - 1;
+    return most < n ? (int)most : n;
+}
 
 __device__ __forceinline__ ExactSpan ex_shared_span(const ExactArgs &a, int rs) {
     ExactSpan s;
     const int tpt = ex_tpt(a.G);
     s.S = a.shared_here ? (a.P + rs - 1) / rs : 0;
-    s.RT = (a.B + tpt - 1) / tpt;
+    s.RT = a.shared_here ? (a.B + tpt - 1) / tpt : 0;
+    s.weight = a.by_items ? min(s.S, 1) : s.S;
     return s;
 }
-// Sequence of n rows and ql tokens. No tile sees more rows than the bound here, and an item has
-// a step even where nothing is visible: it writes zeros.
+// Sequence of n rows and ql tokens. An item has a step even where nothing is visible: it writes
+// zeros.
 __device__ __forceinline__ ExactSpan ex_seq_span(const ExactArgs &a, int n, int ql, int rs) {
     ExactSpan s;
     const int tpt = ex_tpt(a.G);
-    const long long most = (long long)a.sinks + a.window + tpt - 1;
-    const int c = most < n ? (int)most : n;
+    // sinks that a window does not reach start on their own group of 16 rows: up to 15 rows more
+    const int c = ex_most_rows(a.window, a.sinks, tpt, n + 15);
     s.RT = (ql + tpt - 1) / tpt;
-    s.S = s.RT ? max(1, (c + rs - 1) / rs) : 0;
+    s.S = s.RT ? max(1, (min(c, a.window >= n ? n : n + 15) + rs - 1) / rs) : 0;
+    s.weight = a.by_items ? min(s.S, 1) : s.S;
     return s;
 }
 
-// Steps of all items, by one warp (every lane returns the sum).
-__device__ __forceinline__ long long ex_total(const ExactArgs &a, int rs) {
+// Length of the first `seqs` sequences' part of the space, and of the shared part, by one warp
+// (every lane returns the sum).
+__device__ __forceinline__ unsigned ex_length(const ExactArgs &a, int seqs, int rs) {
     const int lane = threadIdx.x & 31;
     const ExactSpan p = ex_shared_span(a, rs);
-    long long t = 0;
+    unsigned t = 0;
     if (!a.lens && !a.q_lens) {
         const ExactSpan s = ex_seq_span(a, a.rows, a.m, rs);
-        t = (long long)a.B * a.H * s.RT * s.S;
+        t = (unsigned)seqs * a.H * s.RT * s.weight;
     } else {
-        for (int b = lane; b < a.B; b += 32) {
+        for (int b = lane; b < seqs; b += 32) {
             const ExactSpan s = ex_seq_span(a, ex_len(a, b), ex_qlen(a, b), rs);
-            t += (long long)a.H * s.RT * s.S;
+            t += (unsigned)a.H * s.RT * s.weight;
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        t = __reduce_add_sync(0xffffffffu, t);
     }
-    return t + (long long)a.H * p.RT * p.S;
+    return t + (unsigned)a.H * p.RT * p.weight;
 }
 
-// First flat step of sequence b's items, by one warp.
-__device__ __forceinline__ long long ex_first(const ExactArgs &a, int b, int rs) {
-    const int lane = threadIdx.x & 31;
-    const ExactSpan p = ex_shared_span(a, rs);
-    long long t = 0;
-    if (!a.lens && !a.q_lens) {
-        const ExactSpan s = ex_seq_span(a, a.rows, a.m, rs);
-        t = (long long)b * a.H * s.RT * s.S;
-    } else {
-        for (int i = lane; i < b; i += 32) {
-            const ExactSpan s = ex_seq_span(a, ex_len(a, i), ex_qlen(a, i), rs);
-            t += (long long)a.H * s.RT * s.S;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    }
-    return t + (long long)a.H * p.RT * p.S;
-}
-
-// Rows per step and threads per block of the split kernel.
+// Rows per step and warps per block of the split kernel.
 constexpr int ex_warps(bool f32_rows) { return f32_rows ? 4 : 8; }
 constexpr int ex_step_rows(bool f32_rows) { return 16 * ex_warps(f32_rows); }
 
-cudaError_t launch_exact_split(const ExactArgs &a, bool f32_rows, bool f32_io, cudaStream_t s);
+cudaError_t launch_exact_split(const ExactArgs &a, const ExactMaps &maps, bool f32_rows, bool f32_io,
+                               cudaStream_t s);
 cudaError_t launch_exact_merge(const ExactArgs &a, bool f32_rows, bool f32_io, cudaStream_t s);
+
+// Clusters of 2, 4 or 8 blocks of the split kernel that the current device runs at once (0: error).
+int exact_split_clusters(int cluster);
+
+// Sticky status of the split kernel's bounded waits on the current device: 0 or 1. Clears it.
+cudaError_t exact_split_status(int *timed_out, cudaStream_t s);
 
 }  // namespace iskv

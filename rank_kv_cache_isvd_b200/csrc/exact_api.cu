@@ -58,6 +58,8 @@ int check_rows(const iskv_exact_rows *r) {
     if (!stride_ok(r->seq_stride, r->batch, e) || !stride_ok(r->head_stride, r->n_kv_heads, e) ||
         !stride_ok(r->row_stride, r->rows, e))
         return ISKV_ERR_INVALID_ARG;
+    // rows of one sequence in one place, or overlapping
+    if (r->rows > 1 && r->row_stride < EX_D) return ISKV_ERR_INVALID_ARG;
     if ((long long)r->batch * r->n_kv_heads > kMaxUnits) return ISKV_ERR_UNSUPPORTED;
     return ISKV_OK;
 }
@@ -78,17 +80,20 @@ int check_queries(const iskv_exact_rows *r, const iskv_exact_queries *q) {
         return ISKV_ERR_INVALID_ARG;
     // float32 rows go with float32 queries and outputs
     if (r->dtype == ISKV_F32 && q->dtype != ISKV_F32) return ISKV_ERR_UNSUPPORTED;
+    // (tile, step) pairs are counted in 32 bits
+    const long long tiles = (q->m + ex_tpt(q->n_q_heads / r->n_kv_heads) - 1) /
+                            ex_tpt(q->n_q_heads / r->n_kv_heads);
+    if ((long long)r->batch * r->n_kv_heads * tiles * (r->rows / 64 + 2) > 0x7fffffffLL)
+        return ISKV_ERR_UNSUPPORTED;
     return ISKV_OK;
 }
 
+// 0 where the items of a dimension all sit in one place: maps then have an extent of 1 there.
+int multiplier(long long stride, int count) { return count > 1 && stride == 0 ? 0 : 1; }
+
 void fill(ExactArgs &a, const iskv_exact_rows *r, const iskv_exact_queries *q, int sms) {
     memset(&a, 0, sizeof(a));
-    const long long e = esz_of(r->dtype), f = esz_of(q->dtype);
-    a.k = static_cast<const char *>(r->k);
-    a.v = static_cast<const char *>(r->v);
-    a.seq_st = r->seq_stride * e;
-    a.head_st = r->head_stride * e;
-    a.row_st = r->row_stride * e;
+    const long long f = esz_of(q->dtype);
     a.B = r->batch;
     a.H = r->n_kv_heads;
     a.rows = r->rows;
@@ -105,8 +110,12 @@ void fill(ExactArgs &a, const iskv_exact_rows *r, const iskv_exact_queries *q, i
     a.m = q->m;
     a.q_lens = q->q_lens;
     a.window = (int)kMaxRows;
+    a.seq_mul = multiplier(r->seq_stride, r->batch);
+    a.head_mul = multiplier(r->head_stride, r->n_kv_heads);
+    a.p_head_mul = 1;
     a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)EX_D));
     a.grid = sms;
+    a.cluster = 1;
 }
 
 // Workspace of the split kernel: its blocks' records, and with `items` one per item as well.
@@ -144,25 +153,49 @@ EncodeTiledFn encode_tiled() {
     return fn;
 }
 
-// 4-D map of bf16 vectors of 128 channels: extents and byte strides of the other dimensions, boxes
-// of 64 channels x box. Shared memory gets 128-byte rows, swizzled. False where the driver does not
-// take it (a stride of 0 over several items, say).
-bool encode_map(CUtensorMap *map, const void *base, const long long (&ext)[3],
-                const long long (&st)[3], const int (&box)[3]) {
+// Map of `n` dimensions: extents, byte strides of all but the first, boxes. The first dimension is
+// 128 bytes of a row; shared memory gets rows of 128 bytes, swizzled.
+bool encode(CUtensorMap *map, int dtype, int n, const void *base, const cuuint64_t *dims,
+            const cuuint64_t *strides, const cuuint32_t *box) {
     const EncodeTiledFn enc = encode_tiled();
-    if (!enc) return false;
-    cuuint64_t dims[4] = {EX_D, 0, 0, 0}, strides[3];
-    cuuint32_t boxes[4] = {64, 0, 0, 0}, steps[4] = {1, 1, 1, 1};
-    for (int i = 0; i < 3; ++i) {
-        dims[i + 1] = (cuuint64_t)ext[i];
-        strides[i] = (cuuint64_t)(ext[i] > 1 ? st[i] : 256);
-        boxes[i + 1] = (cuuint32_t)box[i];
-        if (strides[i] == 0) return false;
-    }
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides,
-               boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t steps[5] = {1, 1, 1, 1, 1};
+    return enc && enc(map, dtype == ISKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                      n, const_cast<void *>(base), dims, strides, box, steps,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows as (channels of a 128-byte part, row, part, kv-head, sequence), boxes of `box_rows` whole
+// rows: [part][row][128 bytes] in shared memory. An extent whose items share one place becomes 1.
+bool rows_map(CUtensorMap *map, const void *base, int dtype, int rows, int heads, int seqs,
+              long long row_st, long long head_st, long long seq_st, int box_rows) {
+    const cuuint64_t e = (cuuint64_t)esz_of(dtype), parts = EX_D * e / 128;
+    auto ext = [](long long st, int n) { return (cuuint64_t)(n > 1 && st == 0 ? 1 : n); };
+    auto str = [](long long st, int n) { return (cuuint64_t)(n > 1 && st ? st : 512); };
+    const cuuint64_t dims[5] = {128 / e, (cuuint64_t)rows, parts, ext(head_st, heads),
+                                ext(seq_st, seqs)};
+    const cuuint64_t strides[4] = {str(row_st * e, rows), 128, str(head_st * e, heads),
+                                   str(seq_st * e, seqs)};
+    const cuuint32_t box[5] = {(cuuint32_t)(128 / e), (cuuint32_t)box_rows, (cuuint32_t)parts, 1, 1};
+    return encode(map, dtype, 5, base, dims, strides, box);
+}
+
+bool own_maps(CUtensorMap *k, CUtensorMap *v, const iskv_exact_rows *r, int box_rows) {
+    if (r->rows == 0) return true;                   // never read
+    return rows_map(k, r->k, r->dtype, r->rows, r->n_kv_heads, r->batch, r->row_stride,
+                    r->head_stride, r->seq_stride, box_rows) &&
+           rows_map(v, r->v, r->dtype, r->rows, r->n_kv_heads, r->batch, r->row_stride,
+                    r->head_stride, r->seq_stride, box_rows);
+}
+bool prefix_maps(CUtensorMap *k, CUtensorMap *v, const iskv_exact_rows *r,
+                 const iskv_exact_prefix *p, int box_rows) {
+    if (p->rows == 0) return true;
+    return rows_map(k, p->k, r->dtype, p->rows, r->n_kv_heads, 1, p->row_stride, p->head_stride, 0,
+                    box_rows) &&
+           rows_map(v, p->v, r->dtype, p->rows, r->n_kv_heads, 1, p->row_stride, p->head_stride, 0,
+                    box_rows);
 }
 
 struct TilePlan {
@@ -221,9 +254,8 @@ TilePlan prefix_plan(const iskv_exact_rows *r, const iskv_exact_queries *q,
     return tile_plan(r->n_kv_heads, r->batch, q->n_q_heads / r->n_kv_heads, p->rows, sms);
 }
 
-// Fills the tile kernel's arguments and maps; false: the rows or queries cannot be mapped.
-bool tile_args(TileArgs &t, CUtensorMap *maps, const TilePlan &p, const ExactArgs &a, bool prefix,
-               float *records) {
+// The tile kernel's arguments.
+void tile_args(TileArgs &t, const TilePlan &p, const ExactArgs &a, bool prefix, float *records) {
     memset(&t, 0, sizeof(t));
     t.B = a.B;
     t.H = a.H;
@@ -234,6 +266,8 @@ bool tile_args(TileArgs &t, CUtensorMap *maps, const TilePlan &p, const ExactArg
     t.m = prefix ? a.B : a.m;
     t.window = a.window;
     t.sinks = a.sinks;
+    t.seq_mul = prefix ? 0 : a.seq_mul;
+    t.head_mul = prefix ? a.p_head_mul : a.head_mul;
     t.tq = p.tq;
     t.pairs = p.pairs;
     t.nsp = p.nsp;
@@ -248,22 +282,56 @@ bool tile_args(TileArgs &t, CUtensorMap *maps, const TilePlan &p, const ExactArg
         t.pre_o = reinterpret_cast<float *>(
             reinterpret_cast<char *>(records) +
             align256((size_t)(prefix ? a.H : a.B * a.H) * p.records * t.m * a.G * 2 * sizeof(float)));
-    if (!encode_map(&maps[0], a.q, {(long long)a.H * a.G, a.m, a.B}, {a.q_head, a.q_tok, a.q_seq},
-                    {a.G, prefix ? 1 : p.tq, prefix ? p.tq : 1}))
-        return false;
-    const char *kv[2] = {prefix ? a.pk : a.k, prefix ? a.pv : a.v};
-    for (int i = 0; i < 2; ++i)
-        if (!encode_map(&maps[1 + i], kv[i], {t.rows, a.H, prefix ? 1 : a.B},
-                        {prefix ? a.p_row : a.row_st, prefix ? a.p_head : a.head_st, a.seq_st},
-                        {TILE_ROWS, 1, 1}))
-            return false;
-    return true;
+}
+// Queries as (64 channels of a half, q-head, token, sequence), boxes of one group's heads and one
+// tile's tokens (prefix: sequences). False where items share a place: the tile kernel cannot take
+// such queries, and the split kernel does.
+bool query_map(CUtensorMap *map, const ExactArgs &a, bool prefix, int tq) {
+    const long long ext[3] = {(long long)a.H * a.G, a.m, a.B}, st[3] = {a.q_head, a.q_tok, a.q_seq};
+    cuuint64_t dims[4] = {EX_D, 0, 0, 0}, strides[3];
+    for (int i = 0; i < 3; ++i) {
+        if (ext[i] > 1 && st[i] == 0) return false;
+        dims[i + 1] = (cuuint64_t)ext[i];
+        strides[i] = (cuuint64_t)(ext[i] > 1 ? st[i] : 256);
+    }
+    const cuuint32_t box[4] = {64, (cuuint32_t)a.G, (cuuint32_t)(prefix ? 1 : tq),
+                               (cuuint32_t)(prefix ? tq : 1)};
+    return encode(map, ISKV_BF16, 4, a.q, dims, strides, box);
 }
 
-int run_split(const ExactArgs &a, const iskv_exact_rows *r, const iskv_exact_queries *q,
+// How the split kernel's work is cut: by items where they fill the GPU well enough (one launch, no
+// records), else by steps. Clusters let few items use more SMs.
+void split_plan(ExactArgs &a, bool f32_rows, int sms) {
+    const int tpt = ex_tpt(a.G), rs = ex_step_rows(f32_rows);
+    const long long tiles = (a.m + tpt - 1) / tpt, items = (long long)a.B * a.H * tiles;
+    const int steps = (ex_most_rows(a.window, a.sinks, tpt, a.rows + 15) + rs - 1) / rs;
+    a.grid = sms;
+    a.cluster = 1;
+    a.by_items = 0;
+    if (a.shared_here) return;                       // its tiles and the sequences' join by records
+    int c = 1;
+    while (c < 8 && items * 2 * c <= sms && steps > c) c *= 2;
+    long long slots = c > 1 ? exact_split_clusters(c) : sms;
+    while (c > 1 && slots < items) {
+        c /= 2;
+        slots = c > 1 ? exact_split_clusters(c) : sms;
+    }
+    if (slots < 1) return;
+    const long long rounds = (items + slots - 1) / slots;
+    // tiles of one prompt see different numbers of rows; long items in the last round leave SMs idle
+    if (tiles > 1 && rounds > 1) return;
+    if (4 * items < 3 * rounds * slots && steps > 8 * c) return;
+    a.by_items = 1;
+    a.cluster = c;
+    a.grid = (int)(items < slots ? items : slots) * c;
+}
+
+int run_split(ExactArgs &a, ExactMaps &maps, const iskv_exact_rows *r, const iskv_exact_queries *q,
               cudaStream_t s) {
     const bool fr = r->dtype == ISKV_F32, fi = q->dtype == ISKV_F32;
-    const int rc = launched(launch_exact_split(a, fr, fi, s));
+    if (!own_maps(&maps.k, &maps.v, r, 16)) return ISKV_ERR_CUDA;
+    split_plan(a, fr, sm_count());
+    const int rc = launched(launch_exact_split(a, maps, fr, fi, s));
     return rc == ISKV_OK ? launched(launch_exact_merge(a, fr, fi, s)) : rc;
 }
 
@@ -300,19 +368,18 @@ extern "C" int iskv_window_attn(const iskv_exact_rows *r, const iskv_exact_queri
     a.sinks = sinks < r->rows ? sinks : r->rows;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const TilePlan p = window_plan(r, q, window, sinks, a.grid);
-    if (p.use) {
+    CUtensorMap qm, km, vm;
+    if (p.use && query_map(&qm, a, false, p.tq)) {
+        if (!own_maps(&km, &vm, r, TILE_ROWS)) return ISKV_ERR_CUDA;
         TileArgs t;
-        CUtensorMap maps[3];
-        if (tile_args(t, maps, p, a, false, p.records > 1 ? static_cast<float *>(ws) : nullptr)) {
-            const int e = launched(
-                launch_exact_tile(t, maps[0], maps[1], maps[2], false, p.alternate, s));
-            if (e != ISKV_OK || p.records == 1) return e;
-            return launched(launch_exact_tile_merge(t, s));
-        }
+        tile_args(t, p, a, false, p.records > 1 ? static_cast<float *>(ws) : nullptr);
+        const int e = launched(launch_exact_tile(t, qm, km, vm, false, p.alternate, s));
+        if (e != ISKV_OK || p.records == 1) return e;
+        return launched(launch_exact_tile_merge(t, s));
     }
-    a.direct = 1;
     a.rec = static_cast<float *>(ws);
-    return run_split(a, r, q, s);
+    ExactMaps maps;
+    return run_split(a, maps, r, q, s);
 }
 
 extern "C" int iskv_mass_decode_workspace(const iskv_exact_rows *r, const iskv_exact_queries *q,
@@ -346,7 +413,8 @@ extern "C" int iskv_mass_decode(const iskv_exact_rows *r, const iskv_exact_queri
     // an empty cache has no weights to add
     a.mass = mass;
     a.mass_out = mass_out;
-    return run_split(a, r, q, reinterpret_cast<cudaStream_t>(stream));
+    ExactMaps maps;
+    return run_split(a, maps, r, q, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int iskv_prefix_decode_workspace(const iskv_exact_rows *r, const iskv_exact_queries *q,
@@ -358,7 +426,8 @@ extern "C" int iskv_prefix_decode_workspace(const iskv_exact_rows *r, const iskv
     const int e = esz_of(r->dtype);
     if (q->m != 1 || q->q_lens || p->rows < 0 || p->rows > kMaxRows ||
         (p->rows > 0 && (!p->k || !p->v)) || !aligned16(p->k) || !aligned16(p->v) ||
-        !stride_ok(p->head_stride, r->n_kv_heads, e) || !stride_ok(p->row_stride, p->rows, e))
+        !stride_ok(p->head_stride, r->n_kv_heads, e) || !stride_ok(p->row_stride, p->rows, e) ||
+        (p->rows > 1 && p->row_stride < EX_D))
         return ISKV_ERR_INVALID_ARG;
     const int sms = sm_count();
     if (!sms) return ISKV_ERR_CUDA;
@@ -380,35 +449,30 @@ extern "C" int iskv_prefix_decode(const iskv_exact_rows *r, const iskv_exact_que
     if (ws_bytes < need) return ISKV_ERR_CAPACITY;
     ExactArgs a;
     fill(a, r, q, sm_count());
-    const long long e = esz_of(r->dtype);
-    a.pk = static_cast<const char *>(p->k);
-    a.pv = static_cast<const char *>(p->v);
-    a.p_head = p->head_stride * e;
-    a.p_row = p->row_stride * e;
     a.P = p->rows;
+    a.p_head_mul = multiplier(p->head_stride, r->n_kv_heads);
     a.rec = static_cast<float *>(ws);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const TilePlan plan = prefix_plan(r, q, p, a.grid);
-    if (plan.use) {
+    ExactMaps maps;
+    CUtensorMap qm, km, vm;
+    if (plan.use && query_map(&qm, a, true, plan.tq)) {
+        if (!prefix_maps(&km, &vm, r, p, TILE_ROWS)) return ISKV_ERR_CUDA;
         const int tpt = ex_tpt(a.G);
-        const size_t at =
-            record_bytes(a.grid, (long long)a.H * (a.B + (a.B + tpt - 1) / tpt));
+        const size_t at = record_bytes(a.grid, (long long)a.H * (a.B + (a.B + tpt - 1) / tpt));
         TileArgs t;
-        CUtensorMap maps[3];
-        if (tile_args(t, maps, plan, a, true,
-                      reinterpret_cast<float *>(static_cast<char *>(ws) + at))) {
-            const int e2 =
-                launched(launch_exact_tile(t, maps[0], maps[1], maps[2], true, plan.alternate, s));
-            if (e2 != ISKV_OK) return e2;
-            a.pre_ml = t.pre_ml;
-            a.pre_o = t.pre_o;
-            a.nsp = plan.records;
-            a.after = 1;
-            return run_split(a, r, q, s);
-        }
+        tile_args(t, plan, a, true, reinterpret_cast<float *>(static_cast<char *>(ws) + at));
+        const int e = launched(launch_exact_tile(t, qm, km, vm, true, plan.alternate, s));
+        if (e != ISKV_OK) return e;
+        a.pre_ml = t.pre_ml;
+        a.pre_o = t.pre_o;
+        a.nsp = plan.records;
+        a.after = 1;
+        return run_split(a, maps, r, q, s);
     }
     a.shared_here = p->rows > 0;
-    return run_split(a, r, q, s);
+    if (!prefix_maps(&maps.pk, &maps.pv, r, p, 16)) return ISKV_ERR_CUDA;
+    return run_split(a, maps, r, q, s);
 }
 
 extern "C" int iskv_evict_workspace(const iskv_exact_rows *r, int budget, size_t *bytes) {
@@ -434,8 +498,7 @@ extern "C" int iskv_evict(const iskv_exact_rows *r, const float *mass, float *ma
         return ISKV_ERR_INVALID_ARG;
     if (r->rows > 0 && (!mass || !mass_out || !pos || !pos_out)) return ISKV_ERR_INVALID_ARG;
     // rows that two units, or two slots, share cannot be moved in place
-    if ((r->batch > 1 && r->seq_stride < EX_D) || (r->n_kv_heads > 1 && r->head_stride < EX_D) ||
-        (r->rows > 1 && r->row_stride < EX_D))
+    if ((r->batch > 1 && r->seq_stride < EX_D) || (r->n_kv_heads > 1 && r->head_stride < EX_D))
         return ISKV_ERR_INVALID_ARG;
     if (ws_bytes < need) return ISKV_ERR_CAPACITY;
     const int sms = sm_count();
@@ -470,8 +533,9 @@ extern "C" int iskv_evict(const iskv_exact_rows *r, const float *mass, float *ma
 }
 
 extern "C" int iskv_exact_status(iskv_stream_t stream) {
-    int timed_out = 0;
-    const int rc =
-        launched(exact_tile_status(&timed_out, reinterpret_cast<cudaStream_t>(stream)));
-    return rc != ISKV_OK ? rc : timed_out ? ISKV_ERR_TIMEOUT : ISKV_OK;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int tile = 0, split = 0;
+    int rc = launched(exact_tile_status(&tile, s));
+    if (rc == ISKV_OK) rc = launched(exact_split_status(&split, s));
+    return rc != ISKV_OK ? rc : tile || split ? ISKV_ERR_TIMEOUT : ISKV_OK;
 }

@@ -82,6 +82,15 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, i
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
         : "memory");
 }
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, int row, int head,
+                                            int seq, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(0), "r"(head), "r"(seq),
+        "r"(smem_u32(bar))
+        : "memory");
+}
 // D[tmem] (+)= A[smem] B[smem]^T and D[tmem] (+)= A[tmem] B[smem]^T, bf16 operands.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -266,9 +275,8 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
                     return false;
                 const int row = w.base(blk);
                 mbar_arrive_expect_tx(&bars->kv_full[st], BLOCK_BYTES);
-                for (int x = 0; x < 2; ++x)
-                    tma_load_4d(ring + st * BLOCK_BYTES + x * HALF_BYTES, map, x * 64, row, w.h, w.b,
-                                &bars->kv_full[st]);
+                tma_load_5d(ring + st * BLOCK_BYTES, map, row, w.h * a.head_mul, w.b * a.seq_mul,
+                            &bars->kv_full[st]);
                 ++issued;
                 return true;
             };

@@ -15,6 +15,7 @@ struct TileArgs {
     const int *lens, *q_lens;
     int m;                             // tokens per sequence (prefix: sequences)
     int window, sinks;
+    int seq_mul, head_mul;             // 0 where all sequences, or kv-heads, share one stream
     int tq;                            // tokens per tile: 128 / G
     int pairs;                         // pairs of tiles per (sequence, kv-head)
     int nsp;                           // splits of the rows' blocks
@@ -26,8 +27,8 @@ struct TileArgs {
     float scale_log2;
 };
 
-// Maps of q (channels, q-heads, tokens, sequences) and of the rows (channels, rows, kv-heads,
-// sequences), boxes of 64 channels.
+// Maps of q (channels, q-heads, tokens, sequences) in boxes of 64 channels, and of the rows (64
+// channels, rows, halves, kv-heads, sequences) in boxes of 128 whole rows.
 cudaError_t launch_exact_tile(const TileArgs &a, const CUtensorMap &q, const CUtensorMap &k,
                               const CUtensorMap &v, bool prefix, bool alternate, cudaStream_t s);
 
