@@ -19,7 +19,7 @@ constexpr int EX_D = 128;
 constexpr int EX_QROWS = 8;            // query rows of a split-kernel tile (tokens x GQA group)
 constexpr int EX_REC = EX_QROWS * (2 + EX_D);   // floats of a record: m[8], l[8], O[8][128]
 constexpr int EX_MAXREC = 1024;        // records that one merge block can combine
-constexpr int EX_PRE_MAX = 256;        // of them at most from the tile kernel
+constexpr int EX_PRE_MAX = 32;         // of them at most from the tile kernel
 
 struct ExactArgs {
     int B, H, rows;
@@ -44,8 +44,11 @@ struct ExactArgs {
     int nsp;                           // their number of splits (0: none)
     float scale_log2;                  // log2(e) / sqrt(128)
     int grid;                          // blocks of the split kernel
-    int cluster;                       // by items: blocks per cluster, which share an item's steps
-    int by_items;                      // 1: a cluster takes whole items; 0: a block takes steps
+    int by_items;                      // 1: a team of warps takes whole items; 0: a block takes steps
+    int team;                          // by items: warps of a team (1, 2, 4, 8) ...
+    int cluster;                       // ... and (team 8) blocks that share an item's steps
+    int rt_max;                        // tiles per (sequence, kv-head) at most
+    unsigned items, share, extra;      // by items: their number, and per team; `extra` teams take 1 more
     int after;                         // 1: launched next to the kernel before it, whose end it awaits
 };
 
@@ -69,17 +72,18 @@ __device__ __forceinline__ int ex_qlen(const ExactArgs &a, int b) {
 // Items in order: the shared prefix's (kv-head, tile of 8 (sequence, q-head) rows), then every
 // sequence's (kv-head, tile of 8 (token, q-head) rows). An item takes S steps of `rs` rows.
 // By steps: the flat space of (item, step) is cut into equal ranges, one per block. By items: the
-// list of items is, one range per cluster, whose blocks share out each item's steps.
+// list of (sequence, kv-head, tile) is, one range per team of warps or cluster of blocks.
 struct ExactSpan {
-    int S;            // steps per item
+    int S;            // steps per item (0: there are no items)
     int RT;           // tiles per kv-head
-    int weight;       // length of an item in the space that is cut: S, or 1
 };
 
-// Rows that a tile of tpt tokens visits at most: its window, and the sinks in groups of 16.
+// Length of the order in which a tile of tpt tokens visits the rows, at most: its window, and the
+// sinks in groups of 32. Sinks that the window does not reach fill up their last group.
 __host__ __device__ inline int ex_most_rows(int window, int sinks, int tpt, int n) {
-    const long long most = (long long)((sinks + 15) & ~15) + window + tpt - 1;
-    return most < n ? (int)most : n;
+    const long long most = (long long)((sinks + 31) & ~31) + window + tpt - 1;
+    const int all = window >= n ? n : n + 31;
+    return most < all ? (int)most : all;
 }
 
 __device__ __forceinline__ ExactSpan ex_shared_span(const ExactArgs &a, int rs) {
@@ -87,7 +91,6 @@ __device__ __forceinline__ ExactSpan ex_shared_span(const ExactArgs &a, int rs) 
     const int tpt = ex_tpt(a.G);
     s.S = a.shared_here ? (a.P + rs - 1) / rs : 0;
     s.RT = a.shared_here ? (a.B + tpt - 1) / tpt : 0;
-    s.weight = a.by_items ? min(s.S, 1) : s.S;
     return s;
 }
 // Sequence of n rows and ql tokens. An item has a step even where nothing is visible: it writes
@@ -95,36 +98,36 @@ __device__ __forceinline__ ExactSpan ex_shared_span(const ExactArgs &a, int rs) 
 __device__ __forceinline__ ExactSpan ex_seq_span(const ExactArgs &a, int n, int ql, int rs) {
     ExactSpan s;
     const int tpt = ex_tpt(a.G);
-    // sinks that a window does not reach start on their own group of 16 rows: up to 15 rows more
-    const int c = ex_most_rows(a.window, a.sinks, tpt, n + 15);
     s.RT = (ql + tpt - 1) / tpt;
-    s.S = s.RT ? max(1, (min(c, a.window >= n ? n : n + 15) + rs - 1) / rs) : 0;
-    s.weight = a.by_items ? min(s.S, 1) : s.S;
+    s.S = s.RT ? max(1, (ex_most_rows(a.window, a.sinks, tpt, n) + rs - 1) / rs) : 0;
     return s;
 }
 
-// Length of the first `seqs` sequences' part of the space, and of the shared part, by one warp
-// (every lane returns the sum).
+// By steps: length of the shared part of the space and of the first `seqs` sequences' part, by one
+// warp (every lane returns the sum).
 __device__ __forceinline__ unsigned ex_length(const ExactArgs &a, int seqs, int rs) {
     const int lane = threadIdx.x & 31;
     const ExactSpan p = ex_shared_span(a, rs);
     unsigned t = 0;
     if (!a.lens && !a.q_lens) {
         const ExactSpan s = ex_seq_span(a, a.rows, a.m, rs);
-        t = (unsigned)seqs * a.H * s.RT * s.weight;
+        t = (unsigned)seqs * a.H * s.RT * s.S;
     } else {
         for (int b = lane; b < seqs; b += 32) {
             const ExactSpan s = ex_seq_span(a, ex_len(a, b), ex_qlen(a, b), rs);
-            t += (unsigned)a.H * s.RT * s.weight;
+            t += (unsigned)a.H * s.RT * s.S;
         }
         t = __reduce_add_sync(0xffffffffu, t);
     }
-    return t + (unsigned)a.H * p.RT * p.weight;
+    return t + (unsigned)a.H * p.RT * p.S;
 }
 
-// Rows per step and warps per block of the split kernel.
-constexpr int ex_warps(bool f32_rows) { return f32_rows ? 4 : 8; }
-constexpr int ex_step_rows(bool f32_rows) { return 16 * ex_warps(f32_rows); }
+// Warps per block of the split kernel, rows per warp and step, rows per step.
+constexpr int EX_WARPS = 8;
+__host__ __device__ constexpr int ex_warp_rows(bool f32_rows) { return f32_rows ? 16 : 32; }
+__host__ __device__ constexpr int ex_step_rows(bool f32_rows) {
+    return EX_WARPS * ex_warp_rows(f32_rows);
+}
 
 cudaError_t launch_exact_split(const ExactArgs &a, const ExactMaps &maps, bool f32_rows, bool f32_io,
                                cudaStream_t s);

@@ -83,7 +83,7 @@ int check_queries(const iskv_exact_rows *r, const iskv_exact_queries *q) {
     // (tile, step) pairs are counted in 32 bits
     const long long tiles = (q->m + ex_tpt(q->n_q_heads / r->n_kv_heads) - 1) /
                             ex_tpt(q->n_q_heads / r->n_kv_heads);
-    if ((long long)r->batch * r->n_kv_heads * tiles * (r->rows / 64 + 2) > 0x7fffffffLL)
+    if ((long long)r->batch * r->n_kv_heads * tiles * (r->rows / 128 + 2) > 0x7fffffffLL)
         return ISKV_ERR_UNSUPPORTED;
     return ISKV_OK;
 }
@@ -122,7 +122,7 @@ void fill(ExactArgs &a, const iskv_exact_rows *r, const iskv_exact_queries *q, i
 size_t record_bytes(int grid, long long items) {
     return align256((size_t)(2LL * grid + items) * EX_REC * sizeof(float));
 }
-long long score_stride(int rows) { return (rows + 15) / 16 * 16; }
+long long score_stride(int rows) { return (rows + 31) / 32 * 32; }
 size_t score_bytes(const iskv_exact_rows *r, int n_q_heads) {
     return align256((size_t)r->batch * n_q_heads * score_stride(r->rows) * sizeof(float));
 }
@@ -200,7 +200,7 @@ bool prefix_maps(CUtensorMap *k, CUtensorMap *v, const iskv_exact_rows *r,
 
 struct TilePlan {
     bool use, alternate;
-    int tq, pairs, nsp, records;
+    int tq, pairs, nsp;
 };
 
 // `tokens` query tokens (prefix: sequences) per unit, over at most `seen` rows each.
@@ -220,15 +220,13 @@ TilePlan tile_plan(int units, int tokens, int G, long long seen, int sms) {
     long long nsp = ctas >= sms ? 1 : sms / ctas;
     const long long most = blocks / 4 > 1 ? blocks / 4 : 1;
     if (nsp > most) nsp = most;
-    if (nsp > EX_PRE_MAX / 2) nsp = EX_PRE_MAX / 2;
-    p.nsp = (int)nsp;
-    p.records = p.nsp * (p.alternate ? 2 : 1);
+    p.nsp = (int)(nsp < EX_PRE_MAX ? nsp : EX_PRE_MAX);
     return p;
 }
 size_t tile_record_bytes(const TilePlan &p, long long units, long long tokens, int G) {
     if (!p.use) return 0;
-    return align256((size_t)(units * p.records * tokens * G) * 2 * sizeof(float)) +
-           align256((size_t)(units * p.records * tokens * G) * EX_D * sizeof(float));
+    return align256((size_t)(units * p.nsp * tokens * G) * 2 * sizeof(float)) +
+           align256((size_t)(units * p.nsp * tokens * G) * EX_D * sizeof(float));
 }
 
 bool all_bf16(const iskv_exact_rows *r, const iskv_exact_queries *q) {
@@ -271,7 +269,6 @@ void tile_args(TileArgs &t, const TilePlan &p, const ExactArgs &a, bool prefix, 
     t.tq = p.tq;
     t.pairs = p.pairs;
     t.nsp = p.nsp;
-    t.records = p.records;
     t.out = a.out;
     t.o_seq = a.o_seq;
     t.o_head = a.o_head;
@@ -281,7 +278,7 @@ void tile_args(TileArgs &t, const TilePlan &p, const ExactArgs &a, bool prefix, 
     if (records)
         t.pre_o = reinterpret_cast<float *>(
             reinterpret_cast<char *>(records) +
-            align256((size_t)(prefix ? a.H : a.B * a.H) * p.records * t.m * a.G * 2 * sizeof(float)));
+            align256((size_t)(prefix ? a.H : a.B * a.H) * p.nsp * t.m * a.G * 2 * sizeof(float)));
 }
 // Queries as (64 channels of a half, q-head, token, sequence), boxes of one group's heads and one
 // tile's tokens (prefix: sequences). False where items share a place: the tile kernel cannot take
@@ -300,36 +297,52 @@ bool query_map(CUtensorMap *map, const ExactArgs &a, bool prefix, int tq) {
 }
 
 // How the split kernel's work is cut: by items where they fill the GPU well enough (one launch, no
-// records), else by steps. Clusters let few items use more SMs.
+// records), else by steps.
 void split_plan(ExactArgs &a, bool f32_rows, int sms) {
-    const int tpt = ex_tpt(a.G), rs = ex_step_rows(f32_rows);
-    const long long tiles = (a.m + tpt - 1) / tpt, items = (long long)a.B * a.H * tiles;
-    const int steps = (ex_most_rows(a.window, a.sinks, tpt, a.rows + 15) + rs - 1) / rs;
+    const int tpt = ex_tpt(a.G), wr = ex_warp_rows(f32_rows);
+    const int tiles = (a.m + tpt - 1) / tpt;
+    const long long items = (long long)a.B * a.H * tiles;
+    const int most = ex_most_rows(a.window, a.sinks, tpt, a.rows);
     a.grid = sms;
     a.cluster = 1;
+    a.team = EX_WARPS;
     a.by_items = 0;
+    a.rt_max = tiles;
     if (a.shared_here) return;                       // its tiles and the sequences' join by records
-    int c = 1;
-    while (c < 8 && items * 2 * c <= sms && steps > c) c *= 2;
-    long long slots = c > 1 ? exact_split_clusters(c) : sms;
-    while (c > 1 && slots < items) {
-        c /= 2;
-        slots = c > 1 ? exact_split_clusters(c) : sms;
+    // teams as large as there are warps for every item, and no larger than the item has rows for
+    int team = EX_WARPS, c = 1;
+    while (team > 1 && (items * team > (long long)sms * EX_WARPS || most <= wr * team / 2)) team /= 2;
+    const int steps = (most + wr * team - 1) / (wr * team);
+    if (team == EX_WARPS)
+        while (c < 8 && items * 2 * c <= sms && steps > c) c *= 2;
+    long long slots = (long long)sms * (EX_WARPS / team);    // teams that run at once
+    for (; c > 1; c /= 2) {
+        slots = exact_split_clusters(c);
+        if (slots >= items) break;
     }
-    if (slots < 1) return;
+    if (c == 1) slots = (long long)sms * (EX_WARPS / team);
     const long long rounds = (items + slots - 1) / slots;
-    // tiles of one prompt see different numbers of rows; long items in the last round leave SMs idle
+    // tiles of one prompt see different numbers of rows; long items in a last, partly filled round
+    // leave SMs idle
     if (tiles > 1 && rounds > 1) return;
     if (4 * items < 3 * rounds * slots && steps > 8 * c) return;
+    const long long teams = items < slots ? items : slots;
     a.by_items = 1;
+    a.team = team;
     a.cluster = c;
-    a.grid = (int)(items < slots ? items : slots) * c;
+    // few items: their teams spread over the SMs
+    const int per_block = EX_WARPS / team;
+    a.grid = (int)((teams + per_block - 1) / per_block) * c;
+    const long long all = (long long)a.grid / c * per_block;
+    a.items = (unsigned)items;
+    a.share = (unsigned)(items / all);
+    a.extra = (unsigned)(items % all);
 }
 
 int run_split(ExactArgs &a, ExactMaps &maps, const iskv_exact_rows *r, const iskv_exact_queries *q,
               cudaStream_t s) {
     const bool fr = r->dtype == ISKV_F32, fi = q->dtype == ISKV_F32;
-    if (!own_maps(&maps.k, &maps.v, r, 16)) return ISKV_ERR_CUDA;
+    if (!own_maps(&maps.k, &maps.v, r, ex_warp_rows(fr))) return ISKV_ERR_CUDA;
     split_plan(a, fr, sm_count());
     const int rc = launched(launch_exact_split(a, maps, fr, fi, s));
     return rc == ISKV_OK ? launched(launch_exact_merge(a, fr, fi, s)) : rc;
@@ -348,7 +361,7 @@ extern "C" int iskv_window_attn_workspace(const iskv_exact_rows *r, const iskv_e
     const TilePlan p = window_plan(r, q, window, sinks, sms);
     const size_t split = record_bytes(sms, 0);
     const size_t tile =
-        p.records > 1 ? tile_record_bytes(p, (long long)r->batch * r->n_kv_heads, q->m,
+        p.nsp > 1 ? tile_record_bytes(p, (long long)r->batch * r->n_kv_heads, q->m,
                                           q->n_q_heads / r->n_kv_heads)
                       : 0;
     *bytes = split > tile ? split : tile;
@@ -372,9 +385,9 @@ extern "C" int iskv_window_attn(const iskv_exact_rows *r, const iskv_exact_queri
     if (p.use && query_map(&qm, a, false, p.tq)) {
         if (!own_maps(&km, &vm, r, TILE_ROWS)) return ISKV_ERR_CUDA;
         TileArgs t;
-        tile_args(t, p, a, false, p.records > 1 ? static_cast<float *>(ws) : nullptr);
+        tile_args(t, p, a, false, p.nsp > 1 ? static_cast<float *>(ws) : nullptr);
         const int e = launched(launch_exact_tile(t, qm, km, vm, false, p.alternate, s));
-        if (e != ISKV_OK || p.records == 1) return e;
+        if (e != ISKV_OK || p.nsp == 1) return e;
         return launched(launch_exact_tile_merge(t, s));
     }
     a.rec = static_cast<float *>(ws);
@@ -466,12 +479,12 @@ extern "C" int iskv_prefix_decode(const iskv_exact_rows *r, const iskv_exact_que
         if (e != ISKV_OK) return e;
         a.pre_ml = t.pre_ml;
         a.pre_o = t.pre_o;
-        a.nsp = plan.records;
+        a.nsp = plan.nsp;
         a.after = 1;
         return run_split(a, maps, r, q, s);
     }
     a.shared_here = p->rows > 0;
-    if (!prefix_maps(&maps.pk, &maps.pv, r, p, 16)) return ISKV_ERR_CUDA;
+    if (!prefix_maps(&maps.pk, &maps.pv, r, p, ex_warp_rows(r->dtype == ISKV_F32))) return ISKV_ERR_CUDA;
     return run_split(a, maps, r, q, s);
 }
 

@@ -19,11 +19,13 @@
 // the outputs lost 4e-6. So each step's products start from zero and are added to the outputs in
 // float32 arithmetic (round to nearest), smallest terms first: 8e-7 at 8 x 32768 rows.
 //
-// By items: a cluster of 1 to 8 blocks shares out an item's steps and joins their results through
-// distributed shared memory: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i. One launch, no
-// workspace. By steps: the flat space of (item, step) is cut into equal ranges, one per block, so
-// that items of any number and lengths fill the GPU evenly; an item that several blocks share
-// leaves one record per block in global memory, which the merge kernel joins in the same way.
+// By items: a team of warps takes whole items. Short ones go to teams of 1, 2 or 4 warps (a block
+// then works on several, and few warps wait for one another), long ones to a block or a cluster of
+// up to 8 blocks that share out the item's steps and join their results through distributed shared
+// memory: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i. One launch, no workspace. By steps: the
+// flat space of (item, step) is cut into equal ranges, one per block, so that items of any number
+// and lengths fill the GPU evenly; an item that several blocks share leaves one record per block in
+// global memory, which the merge kernel joins in the same way.
 #include <math_constants.h>
 #include <string.h>
 
@@ -35,7 +37,9 @@
 namespace iskv {
 namespace {
 
-constexpr int STAGES = 3;
+constexpr int UNITS = 3;               // of a warp's ring: keys, values, keys, ... of its steps
+constexpr int UNIT = 8192;             // bytes: 32 bf16 rows or 16 float32 rows
+constexpr int RED = EX_D + 8;          // stride of joined rows: the warps' stores meet no conflicts
 constexpr uint32_t POLLS = 1u << 18, SUSPEND_NS = 20000;
 
 __device__ int g_split_status;
@@ -153,18 +157,15 @@ __device__ __forceinline__ float4 ldc4(uint32_t a) {
 __device__ __forceinline__ float inverse(float l) { return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l); }
 
 // Where an item's rows and queries are. Its visible rows in an order without the gap between sinks
-// and window: c < skp (sk of them, filled up to a multiple of 16) are the sinks, then the rows from
+// and window: c < skp (sk of them, filled up to a multiple of 32) are the sinks, then the rows from
 // lo on, up to C.
 struct Item {
     int b, h, rt;         // b < 0: shared prefix
-    int weight;
     int n, ql;            // of sequence b
     int C, sk, skp, lo;
-    int S;
     int i0, i1;           // its tokens (sequences, for the shared prefix)
 };
 
-template <int RS>
 __device__ __forceinline__ void geometry(const ExactArgs &a, Item &it) {
     const int tpt = ex_tpt(a.G);
     it.i0 = it.rt * tpt;
@@ -180,220 +181,275 @@ __device__ __forceinline__ void geometry(const ExactArgs &a, Item &it) {
         it.C = hi;
         if (lo > sk) {
             it.sk = sk;
-            it.skp = (sk + 15) & ~15;
+            it.skp = (sk + 31) & ~31;
             it.lo = lo;
             it.C = it.skp + hi - lo;
         }
     }
-    it.S = max(1, (it.C + RS - 1) / RS);
 }
 
-// A position in the list of items: the item, and where the space that is cut begins with it.
-struct Cursor {
+// A way through a share of the work: the item, and the steps [s0, s1) of it to do.
+struct Walk {
     Item it;
-    unsigned first;
-};
+    int s0, s1;
+    unsigned g, end;      // by steps: place in the flat space; by items: number of the item
+    unsigned first;       // by steps: where the item begins
+    int S;                // by steps: its length there
 
-// The item after it: next tile, next kv-head, next sequence with tokens. It must exist.
-template <int RS>
-__device__ __forceinline__ void next_item(const ExactArgs &a, Cursor &c) {
-    Item &it = c.it;
-    c.first += it.weight;
-    const int RT = it.b < 0 ? ex_shared_span(a, RS).RT
-                            : (it.ql + ex_tpt(a.G) - 1) / ex_tpt(a.G);
-    if (++it.rt == RT) {
-        it.rt = 0;
-        if (++it.h == a.H) {
-            it.h = 0;
-            ExactSpan s;
-            do {
-                ++it.b;
-                it.n = ex_len(a, it.b);
-                it.ql = ex_qlen(a, it.b);
-                s = ex_seq_span(a, it.n, it.ql, RS);
-            } while (s.S == 0 && it.b + 1 < a.B);
-            it.weight = s.weight;
-        }
+    // -- by items: `rank` of `parts` blocks does its part of every item
+    __device__ __forceinline__ void settle(const ExactArgs &a, int rs, int rank, int parts) {
+        geometry(a, it);
+        const unsigned n = (unsigned)max(1, (it.C + rs - 1) / rs);
+        s0 = (int)(n * rank / parts);
+        s1 = (int)(n * (rank + 1) / parts);
     }
-    geometry<RS>(a, it);
-}
-
-// The item that place g of the space belongs to (g < its length). By a whole warp.
-template <int RS>
-__device__ __forceinline__ Cursor find_item(const ExactArgs &a, unsigned g) {
-    Cursor c;
-    Item &it = c.it;
-    const int lane = threadIdx.x & 31;
-    const ExactSpan p = ex_shared_span(a, RS);
-    unsigned at = (unsigned)a.H * p.RT * p.weight;
-    int RT = p.RT;
-    if (g < at) {
-        it.b = -1;
-        it.weight = p.weight;
-        it.n = it.ql = 0;
-        at = 0;
-    } else if (!a.lens && !a.q_lens) {
-        const ExactSpan s = ex_seq_span(a, a.rows, a.m, RS);
-        const unsigned each = (unsigned)a.H * s.RT * s.weight;
-        it.b = (int)((g - at) / each);
-        at += it.b * each;
-        it.n = a.rows;
-        it.ql = a.m;
-        it.weight = s.weight;
-        RT = s.RT;
-    } else {
-        it.b = 0;
-        for (int b0 = 0; b0 < a.B; b0 += 32) {
-            const int b = b0 + lane;
-            unsigned len = 0;
-            if (b < a.B) {
-                const ExactSpan s = ex_seq_span(a, ex_len(a, b), ex_qlen(a, b), RS);
-                len = (unsigned)a.H * s.RT * s.weight;
-            }
-            unsigned sum = len;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned x = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += x;
-            }
-            const unsigned past = __ballot_sync(0xffffffffu, at + sum > g);
-            if (past) {
-                const int l = __ffs(past) - 1;
-                it.b = b0 + l;
-                at += __shfl_sync(0xffffffffu, sum - len, l);
-                break;
-            }
-            at += __shfl_sync(0xffffffffu, sum, 31);
-        }
+    __device__ __forceinline__ void seq(const ExactArgs &a) {
         it.n = ex_len(a, it.b);
         it.ql = ex_qlen(a, it.b);
-        const ExactSpan s = ex_seq_span(a, it.n, it.ql, RS);
-        it.weight = s.weight;
-        RT = s.RT;
     }
-    const unsigned i = (g - at) / (unsigned)it.weight;
-    it.h = (int)(i / (unsigned)RT);
-    it.rt = (int)(i - (unsigned)it.h * RT);
-    c.first = at + i * it.weight;
-    geometry<RS>(a, it);
-    return c;
-}
-
-// A block's way through its share: the item, and the steps [s0, s1) of it that are the block's.
-template <int RS>
-struct Walk {
-    Cursor c;
-    unsigned g, end;      // place in the space, end of the share
-    int s0, s1;
-
-    __device__ __forceinline__ void span(const ExactArgs &a, int rank) {
-        if (a.by_items) {
-            s0 = (int)((unsigned)c.it.S * rank / a.cluster);
-            s1 = (int)((unsigned)c.it.S * (rank + 1) / a.cluster);
-        } else {
-            s0 = (int)(g - c.first);
-            s1 = (int)min((unsigned)c.it.weight, s0 + (end - g));
-        }
-    }
-    // To the next item of the share; false: there is none.
-    __device__ __forceinline__ bool next(const ExactArgs &a, int rank) {
-        g += a.by_items ? 1u : (unsigned)(s1 - s0);
+    // Items that have no tokens are passed over. False: the share is done.
+    __device__ __forceinline__ bool begin(const ExactArgs &a, unsigned from, unsigned to, int rs,
+                                          int rank, int parts) {
+        g = from;
+        end = to;
         if (g >= end) return false;
-        next_item<RS>(a, c);
-        span(a, rank);
+        const unsigned unit = g / (unsigned)a.rt_max;
+        it.rt = (int)(g - unit * a.rt_max);
+        it.b = (int)(unit / (unsigned)a.H);
+        it.h = (int)(unit - (unsigned)it.b * a.H);
+        seq(a);
+        while (it.rt * ex_tpt(a.G) >= it.ql)
+            if (!step(a)) return false;
+        settle(a, rs, rank, parts);
+        return true;
+    }
+    __device__ __forceinline__ bool step(const ExactArgs &a) {
+        if (++g >= end) return false;
+        if (++it.rt == a.rt_max) {
+            it.rt = 0;
+            if (++it.h == a.H) {
+                it.h = 0;
+                ++it.b;
+                seq(a);
+            }
+        }
+        return true;
+    }
+
+    // -- by steps
+    __device__ __forceinline__ void cut() {
+        s0 = (int)(g - first);
+        s1 = (int)min((unsigned)S, s0 + (end - g));
+    }
+    // From the item that place g < length of the space belongs to. By a whole warp.
+    __device__ __forceinline__ void begin_steps(const ExactArgs &a, unsigned from, unsigned to, int rs) {
+        g = from;
+        end = to;
+        const int lane = threadIdx.x & 31;
+        const ExactSpan p = ex_shared_span(a, rs);
+        unsigned at = (unsigned)a.H * p.RT * p.S;
+        ExactSpan s = p;
+        if (g < at) {
+            it.b = -1;
+            it.n = it.ql = 0;
+            at = 0;
+        } else if (!a.lens && !a.q_lens) {
+            s = ex_seq_span(a, a.rows, a.m, rs);
+            const unsigned each = (unsigned)a.H * s.RT * s.S;
+            it.b = (int)((g - at) / each);
+            at += it.b * each;
+            it.n = a.rows;
+            it.ql = a.m;
+        } else {
+            it.b = 0;
+            for (int b0 = 0; b0 < a.B; b0 += 32) {
+                const int b = b0 + lane;
+                unsigned len = 0;
+                if (b < a.B) {
+                    const ExactSpan x = ex_seq_span(a, ex_len(a, b), ex_qlen(a, b), rs);
+                    len = (unsigned)a.H * x.RT * x.S;
+                }
+                unsigned sum = len;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const unsigned x = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += x;
+                }
+                const unsigned past = __ballot_sync(0xffffffffu, at + sum > g);
+                if (past) {
+                    const int l = __ffs(past) - 1;
+                    it.b = b0 + l;
+                    at += __shfl_sync(0xffffffffu, sum - len, l);
+                    break;
+                }
+                at += __shfl_sync(0xffffffffu, sum, 31);
+            }
+            seq(a);
+            s = ex_seq_span(a, it.n, it.ql, rs);
+        }
+        S = s.S;
+        const unsigned i = (g - at) / (unsigned)S;
+        it.h = (int)(i / (unsigned)s.RT);
+        it.rt = (int)(i - (unsigned)it.h * s.RT);
+        first = at + i * S;
+        geometry(a, it);
+        cut();
+    }
+
+    // To the next item of the share; false: there is none.
+    __device__ __forceinline__ bool next(const ExactArgs &a, int rs, int rank, int parts) {
+        if (a.by_items) {
+            do {
+                if (!step(a)) return false;
+            } while (it.rt * ex_tpt(a.G) >= it.ql);
+            settle(a, rs, rank, parts);
+            return true;
+        }
+        g += (unsigned)(s1 - s0);
+        if (g >= end) return false;
+        first += S;
+        const int RT = it.b < 0 ? ex_shared_span(a, rs).RT
+                                : (it.ql + ex_tpt(a.G) - 1) / ex_tpt(a.G);
+        if (++it.rt == RT) {
+            it.rt = 0;
+            if (++it.h == a.H) {
+                it.h = 0;
+                ExactSpan s;
+                do {
+                    ++it.b;
+                    seq(a);
+                    s = ex_seq_span(a, it.n, it.ql, rs);
+                } while (s.S == 0 && it.b + 1 < a.B);
+                S = s.S;
+            }
+        }
+        geometry(a, it);
+        cut();
         return true;
     }
 };
 
 template <bool F32ROWS, bool F32IO, bool MASS>
-__global__ void __launch_bounds__(32 * ex_warps(F32ROWS), 1)
+__global__ void __launch_bounds__(32 * EX_WARPS, 1)
 exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ ExactMaps maps) {
-    constexpr int W = ex_warps(F32ROWS);
-    constexpr int RS = ex_step_rows(F32ROWS);
-    constexpr int HALF = 16 * (F32ROWS ? 512 : 256); // keys of a stage, then as much of values
-    constexpr int STAGE = 2 * HALF;
+    constexpr int WR = ex_warp_rows(F32ROWS);
+    constexpr int NT = WR / 8;                       // groups of 8 rows: columns of a product S
     constexpr int PARTS = F32ROWS ? 4 : 2;           // 128-byte parts of a row
+    constexpr int PART = UNIT / PARTS;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
-    float *red = reinterpret_cast<float *>(smem + W * STAGES * STAGE);   // [W][8][128]
-    float *red_m = red + W * EX_QROWS * EX_D, *red_l = red_m + W * EX_QROWS;
-    float *sum_m = red_l + W * EX_QROWS, *sum_l = sum_m + EX_QROWS;      // [8] each
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sum_l + EX_QROWS);     // [W][STAGES]
-    const uint32_t ring = smem_u32(smem) + warp * STAGES * STAGE;
-    const uint32_t bar = smem_u32(bars) + warp * STAGES * 8;
+    float *red = reinterpret_cast<float *>(smem + EX_WARPS * UNITS * UNIT);   // [8][8][RED]
+    float *red_m = red + EX_WARPS * EX_QROWS * RED, *red_l = red_m + EX_WARPS * EX_QROWS;  // [8][8]
+    float *sum_m = red_l + EX_WARPS * EX_QROWS, *sum_l = sum_m + EX_QROWS;    // [8], of a block
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sum_l + EX_QROWS);          // [8][UNITS]
+    const uint32_t ring = smem_u32(smem) + warp * UNITS * UNIT;
+    const uint32_t bar = smem_u32(bars) + warp * UNITS * 8;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (lane == 0) {
+        if (a.rows > 0) {                            // the first copies then find the maps at hand
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k))
+                         : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v))
+                         : "memory");
+        }
 #pragma unroll
-        for (int i = 0; i < STAGES; ++i) mbar_init(bars + warp * STAGES + i, 1);
+        for (int i = 0; i < UNITS; ++i) mbar_init(bars + warp * UNITS + i, 1);
         fence_mbar_init();
     }
     __syncwarp();
-    const int rank = a.cluster > 1 ? (int)(blockIdx.x % (unsigned)a.cluster) : 0;
-    const unsigned length = ex_length(a, a.B, RS);
-    const unsigned shares = (unsigned)a.grid / a.cluster, share = blockIdx.x / a.cluster;
-    Walk<RS> w;
+    // teams of T warps, tw of which this one is; `parts` blocks of a cluster share an item
+    const int T = a.team, tw = warp & (T - 1), team0 = warp - tw;
+    const int rs = WR * T;
+    const int parts = a.by_items ? a.cluster : 1;
+    const int rank = parts > 1 ? (int)(blockIdx.x & (unsigned)(parts - 1)) : 0;
+    auto team_sync = [&]() {
+        if (T == EX_WARPS) __syncthreads();
+        else if (T == 1) __syncwarp();
+        else asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / T), "r"(32 * T) : "memory");
+    };
+    Walk w;
+    bool have;
     if (a.by_items) {
-        w.g = (unsigned)((unsigned long long)length * share / shares);
-        w.end = (unsigned)((unsigned long long)length * (share + 1) / shares);
+        const unsigned team = (blockIdx.x / (unsigned)parts) * (EX_WARPS / T) + warp / T;
+        const unsigned from = team * a.share + min(team, a.extra);
+        have = w.begin(a, from, min(a.items, from + a.share + (team < a.extra ? 1u : 0u)), rs, rank,
+                       parts);
     } else {
-        const unsigned per = (length + shares - 1) / shares;
-        w.g = min(length, share * per);
-        w.end = min(length, w.g + per);
+        const unsigned length = ex_length(a, a.B, rs);
+        const unsigned per = (length + a.grid - 1) / a.grid, from = blockIdx.x * per;
+        have = from < length;
+        if (have) w.begin_steps(a, from, min(length, from + per), rs);
     }
     bool late = false;                               // a wait hit its bound
-    if (w.g < w.end) {
-        w.c = find_item<RS>(a, w.g);
-        w.span(a, rank);
-        Walk<RS> nw = w;                             // what is loaded next: nw's step `ns`
-        int ns = nw.s0, ld_stage = 0, ld_count = 0;
+    if (have) {
+        Walk nw = w;                                 // what is loaded next: nw's step `ns`, keys
+        int ns = nw.s0, loads = 0;                   // first (`loads` even), then values
+        uint32_t ld_at = 0;
         bool more = true;
-        // Fills one stage, with this warp's rows of the next step that has any.
+        // Queries into L2, ahead of the rows' copies: they are read when the item begins.
+        auto bring_queries = [&](const Item &it) {
+            const int row = lane >> 2, line = lane & 3, i = it.i0 + row / a.G;
+            if (i < it.i1 && (F32IO || line < 2))
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                    a.q + (it.b < 0 ? i : it.b) * a.q_seq + (it.h * a.G + row % a.G) * a.q_head +
+                    (it.b < 0 ? 0 : i) * a.q_tok + line * 128));
+        };
+        bring_queries(nw.it);
+        // Fills one unit of the ring with this warp's rows of the next step that has any.
         auto load = [&]() {
             while (more) {
                 while (ns >= nw.s1) {
-                    more = nw.next(a, rank);
+                    more = nw.next(a, rs, rank, parts);
                     if (!more) return;
                     ns = nw.s0;
+                    bring_queries(nw.it);
                 }
-                const Item &it = nw.c.it;
-                const int c0 = ns * RS + warp * 16;
-                ++ns;
-                if (c0 >= it.C) continue;
+                const Item &it = nw.it;
+                const int c0 = ns * rs + tw * WR;
+                if (c0 >= it.C) {
+                    ++ns;
+                    continue;
+                }
                 if (lane == 0) {
                     const int row = c0 < it.skp ? c0 : c0 - it.skp + it.lo;
-                    const uint32_t dst = ring + ld_stage * STAGE, b = bar + ld_stage * 8;
+                    const uint32_t b = bar + ld_at * 8;
+                    const CUtensorMap *map = it.b < 0 ? (loads & 1 ? &maps.pv : &maps.pk)
+                                                      : (loads & 1 ? &maps.v : &maps.k);
                     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(b),
-                                 "r"(STAGE)
+                                 "r"(UNIT)
                                  : "memory");
-                    if (it.b < 0) {
-                        tma_load_5d(dst, &maps.pk, row, it.h * a.p_head_mul, 0, b);
-                        tma_load_5d(dst + HALF, &maps.pv, row, it.h * a.p_head_mul, 0, b);
-                    } else {
-                        tma_load_5d(dst, &maps.k, row, it.h * a.head_mul, it.b * a.seq_mul, b);
-                        tma_load_5d(dst + HALF, &maps.v, row, it.h * a.head_mul, it.b * a.seq_mul, b);
-                    }
+                    tma_load_5d(ring + ld_at * UNIT, map, row,
+                                it.h * (it.b < 0 ? a.p_head_mul : a.head_mul),
+                                it.b < 0 ? 0 : it.b * a.seq_mul, b);
                 }
-                ++ld_count;
-                ld_stage = ld_stage + 1 == STAGES ? 0 : ld_stage + 1;
+                ns += loads & 1;
+                ++loads;
+                ld_at = ld_at + 1 == UNITS ? 0 : ld_at + 1;
                 return;
             }
         };
 #pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i) load();
+        for (int i = 0; i < UNITS; ++i) load();
 
         // fragment addresses: 128-byte rows of a part, whose 16-byte chunks are permuted by row
         const int kr = (lane & 7) + ((lane >> 4) << 3), vr = lane & 15;
         const uint32_t k_at = kr * 128 + ((((lane >> 3) & 1) ^ (kr & 7)) << 4);
         const uint32_t v_at = vr * 128 + (((lane >> 4) ^ (vr & 7)) << 4);
-        int stage = 0;
-        uint32_t parity = 0;
+        uint32_t unit = 0, parity = 0;
+        auto taken = [&]() {                         // the unit in use is free: refill it
+            __syncwarp();
+            load();
+            if (++unit == UNITS) {
+                unit = 0;
+                parity ^= 1;
+            }
+        };
         const int tok = g / a.G, head = g - tok * a.G;
 
-        bool have = true;
         while (have) {
-            const Item it = w.c.it;
+            const Item it = w.it;
             uint32_t qh[8][2], qm[F32IO ? 8 : 1][2], ql[F32IO ? 8 : 1][2];
             float2 o[16];
             float m = -CUDART_INF_F, l = 0.f;
@@ -423,92 +479,111 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
             const bool plain = it.b < 0 || it.i1 - it.i0 == 1;
 
             for (int st = w.s0; st < w.s1; ++st) {
-                const int c0 = st * RS + warp * 16;
+                const int c0 = st * rs + tw * WR;
                 if (c0 >= it.C) continue;
-                load();
-                late |= !wait_for(bar + stage * 8, parity);
-                const uint32_t kb_ = ring + stage * STAGE, vb_ = kb_ + HALF;
                 const bool sinks = c0 < it.skp;
-                const int seen = min(16, (sinks ? it.sk : it.C) - c0);   // rows with a row behind
-                if (seen < 16) {
-                    // values of rows that nobody sees may be anything: 0 x NaN would reach o
-                    for (int r = seen; r < 16; ++r)
-                        if (lane < 8 * PARTS)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                             vb_ + (lane >> 3) * 2048 + r * 128 + (lane & 7) * 16),
-                                         "r"(0)
-                                         : "memory");
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                float s[2][4];
+                const int seen = min(WR, (sinks ? it.sk : it.C) - c0);   // rows with a row behind
+                late |= !wait_for(bar + unit * 8, parity);
+                const uint32_t kb_ = ring + unit * UNIT;
+                float s[NT][2];                      // scores of row g at columns 8 nt + 2 t + x
                 if constexpr (!F32ROWS) {
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) {
-                        uint32_t kb[4];
-                        ldsm4(kb_ + (ks >> 2) * 2048 + (k_at ^ ((ks & 3) << 5)), kb);
-#pragma unroll
-                        for (int nt = 0; nt < 2; ++nt) {
-                            const uint32_t b0 = kb[2 * nt], b1 = kb[2 * nt + 1];
-                            if constexpr (F32IO) {
-                                if (ks == 0) mma0(s[nt], ql[ks][0], 0u, ql[ks][1], 0u, b0, b1);
-                                else mma(s[nt], ql[ks][0], 0u, ql[ks][1], 0u, b0, b1);
-                                mma(s[nt], qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], b0, b1);
-                            } else {
-                                if (ks == 0) mma0(s[nt], qh[ks][0], 0u, qh[ks][1], 0u, b0, b1);
-                                else mma(s[nt], qh[ks][0], 0u, qh[ks][1], 0u, b0, b1);
-                            }
-                        }
-                    }
-                } else {
+                    // two chains of products per 8 rows, so that few wait on one another
+                    float c[NT][4], e[F32IO ? NT : 1][4];
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
-                        for (int nt = 0; nt < 2; ++nt) {
-                            uint32_t kh[2], km[2], kl[2];
-                            const int r = nt * 8 + g;
+                        for (int np = 0; np < NT / 2; ++np) {
+                            uint32_t kb[4];
+                            ldsm4(kb_ + (ks >> 2) * PART + np * 2048 + (k_at ^ ((ks & 3) << 5)), kb);
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const int ch = ((ks & 1) * 4 + 2 * x + (t >> 1)) ^ (r & 7);
-                                const float2 f = lds2(kb_ + (ks >> 1) * 2048 + r * 128 + ch * 16 +
-                                                      (t & 1) * 8);
-                                split3(f.x, f.y, kh[x], km[x], kl[x]);
+                            for (int y = 0; y < 2; ++y) {
+                                const int nt = 2 * np + y;
+                                const uint32_t b0 = kb[2 * y], b1 = kb[2 * y + 1];
+                                if constexpr (F32IO) {
+                                    if (ks == 0) {
+                                        mma0(e[nt], ql[ks][0], 0u, ql[ks][1], 0u, b0, b1);
+                                        mma0(c[nt], qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], b0, b1);
+                                    } else {
+                                        mma(e[nt], ql[ks][0], 0u, ql[ks][1], 0u, b0, b1);
+                                        mma(c[nt], qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], b0, b1);
+                                    }
+                                } else {
+                                    if (ks == 0) mma0(c[nt], qh[ks][0], 0u, qh[ks][1], 0u, b0, b1);
+                                    else mma(c[nt], qh[ks][0], 0u, qh[ks][1], 0u, b0, b1);
+                                }
                             }
-                            if (ks == 0)
-                                mma0(s[nt], qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], kl[0], kl[1]);
-                            else
-                                mma(s[nt], qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], kl[0], kl[1]);
-                            mma(s[nt], ql[ks][0], 0u, ql[ks][1], 0u, kh[0], kh[1]);
-                            mma(s[nt], qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], km[0], km[1]);
-                            mma(s[nt], qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], kh[0], kh[1]);
                         }
+                    // rows 8-15 hold the mid terms' sums
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            s[nt][x] = F32IO ? (e[nt][x] + c[nt][2 + x]) + c[nt][x] : c[nt][x];
+                } else {
+                    // the large products restart every 32 channels and are summed in float32
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float e[4];                  // the small ones
+                        s[nt][0] = s[nt][1] = 0.f;
+#pragma unroll
+                        for (int kp = 0; kp < 4; ++kp) {
+                            float c[4];
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const int ks = 2 * kp + y, r = nt * 8 + g;
+                                uint32_t kh[2], km[2], kl[2];
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    const int ch = (y * 4 + 2 * x + (t >> 1)) ^ (r & 7);
+                                    const float2 f =
+                                        lds2(kb_ + kp * PART + r * 128 + ch * 16 + (t & 1) * 8);
+                                    split3(f.x, f.y, kh[x], km[x], kl[x]);
+                                }
+                                if (ks == 0)
+                                    mma0(e, qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], kl[0], kl[1]);
+                                else
+                                    mma(e, qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], kl[0], kl[1]);
+                                mma(e, ql[ks][0], 0u, ql[ks][1], 0u, kh[0], kh[1]);
+                                mma(e, qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], km[0], km[1]);
+                                if (y == 0)
+                                    mma0(c, qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], kh[0], kh[1]);
+                                else
+                                    mma(c, qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], kh[0], kh[1]);
+                            }
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) s[nt][x] += c[x] + c[2 + x];
+                        }
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) s[nt][x] += e[x] + e[2 + x];
+                    }
                 }
-                // scores of row g at 8 nt + 2 t + x of the 16 (rows 8-15 hold the mid terms' sums)
-                float p[2][2];
+                taken();
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        p[nt][x] = (s[nt][x] + s[nt][2 + x]) * a.scale_log2;
-                if (seen < 16 || !plain) {
+                    for (int x = 0; x < 2; ++x) s[nt][x] *= a.scale_log2;
+                if (seen < WR || !plain) {
                     const int row0 = sinks ? c0 : c0 - it.skp + it.lo;
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             const int r = 8 * nt + 2 * t + x, j = row0 + r;
                             const bool see = r < seen && (plain || (j <= pos && (j < a.sinks ||
                                                                     j > pos - a.window)));
-                            if (!see) p[nt][x] = -CUDART_INF_F;
+                            if (!see) s[nt][x] = -CUDART_INF_F;
                         }
                 }
-                float top = fmaxf(fmaxf(p[0][0], p[0][1]), fmaxf(p[1][0], p[1][1]));
+                float top = -CUDART_INF_F;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) top = fmaxf(top, fmaxf(s[nt][0], s[nt][1]));
                 if constexpr (MASS) {
                     if (g < a.G) {
                         float *sc = a.scores +
                                     (((long long)it.b * a.H + it.h) * a.G + g) * a.score_st + c0 + 2 * t;
-                        *reinterpret_cast<float2 *>(sc) = make_float2(p[0][0], p[0][1]);
-                        *reinterpret_cast<float2 *>(sc + 8) = make_float2(p[1][0], p[1][1]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            *reinterpret_cast<float2 *>(sc + 8 * nt) = make_float2(s[nt][0], s[nt][1]);
                     }
                 }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -528,29 +603,52 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                     }
                 }
                 const float ref = m == -CUDART_INF_F ? 0.f : m;
+                uint32_t ph[NT], pm[NT], pl[NT];
+                float add = 0.f;
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) p[nt][x] = ex2(p[nt][x] - ref);
-                l += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
-                uint32_t ph[2], pm[2], pl[2];
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-                    split3(p[nt][0], p[nt][1], ph[nt], pm[nt], pl[nt]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float x = ex2(s[nt][0] - ref), y = ex2(s[nt][1] - ref);
+                    add += x + y;
+                    split3(x, y, ph[nt], pm[nt], pl[nt]);
+                }
+                l += add;
+
+                late |= !wait_for(bar + unit * 8, parity);
+                const uint32_t vb_ = ring + unit * UNIT;
+                if (seen < WR) {
+                    // values of rows that nobody sees may be anything: 0 x NaN would reach o
+                    for (int r = seen; r < WR; ++r)
+                        if (lane < 8 * PARTS)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             vb_ + (lane >> 3) * PART + r * 128 + (lane & 7) * 16),
+                                         "r"(0)
+                                         : "memory");
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
                 if constexpr (!F32ROWS) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        uint32_t vb[4];
-                        ldsm4t(vb_ + (i >> 2) * 2048 + (v_at ^ ((i & 3) << 5)), vb);
+                        uint32_t vb[NT / 2][4];
+#pragma unroll
+                        for (int kp = 0; kp < NT / 2; ++kp)
+                            ldsm4t(vb_ + (i >> 2) * PART + kp * 2048 + (v_at ^ ((i & 3) << 5)), vb[kp]);
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            const uint32_t b0 = vb[2 * x], b1 = vb[2 * x + 1];
                             float c[4];
                             if constexpr (F32IO) {
-                                mma0(c, pl[0], 0u, pl[1], 0u, b0, b1);
-                                mma(c, ph[0], pm[0], ph[1], pm[1], b0, b1);
-                            } else {
-                                mma0(c, ph[0], pm[0], ph[1], pm[1], b0, b1);
+#pragma unroll
+                                for (int kp = 0; kp < NT / 2; ++kp) {
+                                    const uint32_t b0 = vb[kp][2 * x], b1 = vb[kp][2 * x + 1];
+                                    if (kp == 0) mma0(c, pl[0], 0u, pl[1], 0u, b0, b1);
+                                    else mma(c, pl[2 * kp], 0u, pl[2 * kp + 1], 0u, b0, b1);
+                                }
+                            }
+#pragma unroll
+                            for (int kp = 0; kp < NT / 2; ++kp) {
+                                const uint32_t b0 = vb[kp][2 * x], b1 = vb[kp][2 * x + 1];
+                                if (kp == 0 && !F32IO) mma0(c, ph[0], pm[0], ph[1], pm[1], b0, b1);
+                                else mma(c, ph[2 * kp], pm[2 * kp], ph[2 * kp + 1], pm[2 * kp + 1], b0, b1);
                             }
                             o[2 * i + x] = add2(o[2 * i + x],
                                                 add2(make_float2(c[0], c[1]), make_float2(c[2], c[3])));
@@ -567,7 +665,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                             for (int y = 0; y < 2; ++y) {
                                 const int r = 8 * x + 2 * t + y;
                                 const int ch = ((i & 3) * 2 + (g >> 2)) ^ (r & 7);
-                                f[y] = lds1(vb_ + (i >> 2) * 2048 + r * 128 + ch * 16 + (g & 3) * 4);
+                                f[y] = lds1(vb_ + (i >> 2) * PART + r * 128 + ch * 16 + (g & 3) * 4);
                             }
                             split3(f[0], f[1], vh[x], vm[x], vl[x]);
                         }
@@ -579,158 +677,226 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                         o[i] = add2(o[i], add2(make_float2(c[0], c[1]), make_float2(c[2], c[3])));
                     }
                 }
-                __syncwarp();                        // the stage may be refilled by the next load
-                if (++stage == STAGES) {
-                    stage = 0;
-                    parity ^= 1;
-                }
+                taken();
             }
 
-            // ---- this block's part of the item is complete: join the warps ----------------------
+            // ---- the team's part of the item is complete: join its warps ------------------------
             l += __shfl_xor_sync(0xffffffffu, l, 1);
             l += __shfl_xor_sync(0xffffffffu, l, 2);
-            float *mine = red + (warp * EX_QROWS + g) * EX_D + 2 * t;
+            float *mine = red + (warp * EX_QROWS + g) * RED + 2 * t;
 #pragma unroll
             for (int i = 0; i < 16; ++i) *reinterpret_cast<float2 *>(mine + 8 * i) = o[i];
             if (t == 0) {
                 red_m[warp * EX_QROWS + g] = m;
                 red_l[warp * EX_QROWS + g] = l;
             }
-            __syncthreads();
-            // Whole items end here; parts leave a record. A record's place: the block's, 0 where
-            // the item began before it and 1 where it goes on behind it, or (whole, but joined with
-            // other records or weights) the item's.
-            const bool whole = a.by_items || (w.s0 == 0 && w.s1 == it.weight);
-            const bool finish = a.by_items || (whole && !MASS && !a.shared_here && !a.nsp);
-            long long slot = 2LL * blockIdx.x + (w.s0 == 0 ? 1 : 0);
-            if (whole) {
-                const int RT = ex_shared_span(a, RS).RT;
-                slot = 2LL * a.grid + (it.b < 0 ? it.h * RT + it.rt : a.H * RT + it.b * a.H + it.h);
+            team_sync();
+            // A part of an item leaves a record: the block's, 0 where the item began before it and 1
+            // where it goes on behind it; or the item's, where other records join it.
+            const bool whole = a.by_items || (w.s0 == 0 && w.s1 == w.S);
+            const bool finish = a.by_items || (whole && !MASS && !a.shared_here);
+            int slot = 2 * blockIdx.x + (w.s0 == 0 ? 1 : 0);
+            if (!finish && whole) {
+                const int RT = ex_shared_span(a, rs).RT;
+                slot = 2 * a.grid + (it.b < 0 ? it.h * RT + it.rt : a.H * RT + it.b * a.H + it.h);
             }
-            for (int e = threadIdx.x; e < EX_QROWS * EX_D / 4; e += 32 * W) {
-                const int r = e / (EX_D / 4), d = (e % (EX_D / 4)) * 4;
-                float M = -CUDART_INF_F;
+            // a warp per query row, four channels per lane
+            auto write = [&](int r, const float4 &y, float L) {
+                const int tk = it.i0 + r / a.G, hd = r % a.G;
+                if (r / a.G >= ex_tpt(a.G) || tk >= it.i1) return;
+                const float inv = inverse(L);
+                char *op = a.out + it.b * a.o_seq + (it.h * a.G + hd) * a.o_head + tk * a.o_tok;
+                if constexpr (F32IO)
+                    *reinterpret_cast<float4 *>(op + lane * 16) =
+                        make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+                else
+                    *reinterpret_cast<uint2 *>(op + lane * 8) =
+                        make_uint2(pack(y.x * inv, y.y * inv), pack(y.z * inv, y.w * inv));
+            };
+            const int nsp = finish ? a.nsp : 0;
+            if (nsp) asm volatile("griddepcontrol.wait;" ::: "memory");
+            const int used = ex_tpt(a.G) * a.G;
+            for (int r = tw; r < (finish ? used : EX_QROWS); r += T) {
+                float M = -CUDART_INF_F, mx[EX_WARPS];
 #pragma unroll
-                for (int x = 0; x < W; ++x) M = fmaxf(M, red_m[x * EX_QROWS + r]);
+                for (int x = 0; x < EX_WARPS; ++x) {
+                    mx[x] = x < T ? red_m[(team0 + x) * EX_QROWS + r] : -CUDART_INF_F;
+                    M = fmaxf(M, mx[x]);
+                }
+                // the tile kernel's records of this row: lane x has record x
+                float pm_ = -CUDART_INF_F, pl_ = 0.f;
+                const long long pre = ((long long)it.h * a.nsp * a.B + it.b) * a.G + r;
+                const long long pre_st = (long long)a.B * a.G;
+                if (nsp) {
+                    if (lane < nsp) {
+                        const float2 ml = __ldcg(
+                            reinterpret_cast<const float2 *>(a.pre_ml + 2 * (pre + lane * pre_st)));
+                        pm_ = ml.x;
+                        pl_ = ml.y;
+                    }
+                    float top = pm_;
+#pragma unroll
+                    for (int x = 16; x > 0; x >>= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                    M = fmaxf(M, top);
+                }
                 const float ref = M == -CUDART_INF_F ? 0.f : M;
                 float L = 0.f;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int x = 0; x < W; ++x) {
-                    const float f = ex2(red_m[x * EX_QROWS + r] - ref);
-                    const float4 y = *reinterpret_cast<const float4 *>(
-                        red + (x * EX_QROWS + r) * EX_D + d);
-                    L += f * red_l[x * EX_QROWS + r];
-                    acc.x += f * y.x;
-                    acc.y += f * y.y;
-                    acc.z += f * y.z;
-                    acc.w += f * y.w;
+                for (int x = 0; x < EX_WARPS; ++x) {
+                    if (x >= T) break;
+                    const float f = ex2(mx[x] - ref);
+                    const float4 v = *reinterpret_cast<const float4 *>(
+                        red + ((team0 + x) * EX_QROWS + r) * RED + lane * 4);
+                    L += f * red_l[(team0 + x) * EX_QROWS + r];
+                    y.x += f * v.x;
+                    y.y += f * v.y;
+                    y.z += f * v.z;
+                    y.w += f * v.w;
                 }
-                if (finish) {
-                    // the sum replaces warp 0's part, which this thread alone reads
-                    *reinterpret_cast<float4 *>(red + r * EX_D + d) = acc;
-                    if (d == 0) {
+                if (nsp) {
+                    const float f = ex2(pm_ - ref);
+                    float add = f * pl_;
+#pragma unroll
+                    for (int x = 16; x > 0; x >>= 1) add += __shfl_xor_sync(0xffffffffu, add, x);
+                    L += add;
+#pragma unroll 6
+                    for (int x = 0; x < nsp; ++x) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(
+                            a.pre_o + (pre + x * pre_st) * EX_D + lane * 4));
+                        const float fx = __shfl_sync(0xffffffffu, f, x);
+                        y.x += fx * v.x;
+                        y.y += fx * v.y;
+                        y.z += fx * v.z;
+                        y.w += fx * v.w;
+                    }
+                }
+                if (finish && parts == 1) {
+                    write(r, y, L);
+                    if (MASS && lane == 0) {
+                        // (reference, sum) of the row for the weights below
+                        red_m[team0 * EX_QROWS + r] = ref;
+                        red_l[team0 * EX_QROWS + r] = L;
+                    }
+                } else if (finish) {
+                    // the sum replaces the first warp's part, which this warp alone reads
+                    *reinterpret_cast<float4 *>(red + r * RED + lane * 4) = y;
+                    if (lane == 0) {
                         sum_m[r] = M;
                         sum_l[r] = L;
                     }
                 } else {
-                    float *rec = a.rec + slot * EX_REC;
-                    if (d == 0) {
+                    float *rec = a.rec + (long long)slot * EX_REC;
+                    if (lane == 0) {
                         rec[r] = M;
                         rec[EX_QROWS + r] = L;
                     }
-                    *reinterpret_cast<float4 *>(rec + 2 * EX_QROWS + r * EX_D + d) = acc;
+                    *reinterpret_cast<float4 *>(rec + 2 * EX_QROWS + r * EX_D + lane * 4) = y;
                 }
             }
-            __syncthreads();
-            if (finish) {
-                if (a.cluster > 1) cluster_sync();
-                if (a.nsp) asm volatile("griddepcontrol.wait;" ::: "memory");
-                const int c = a.by_items ? a.cluster : 1;
-                const uint32_t red_a = smem_u32(red), m_a = smem_u32(sum_m), l_a = smem_u32(sum_l);
-                constexpr int E = EX_QROWS * EX_D / 4;
-                // the cluster's blocks share out the outputs
-                for (int e = E * rank / c + threadIdx.x; e < E * (rank + 1) / c; e += 32 * W) {
-                    const int r = e / (EX_D / 4), d = (e % (EX_D / 4)) * 4;
-                    const int tk = it.i0 + r / a.G, hd = r % a.G;
-                    if (r / a.G >= ex_tpt(a.G) || tk >= it.i1) continue;
-                    float M = -CUDART_INF_F;
-                    for (int x = 0; x < c; ++x) M = fmaxf(M, ldc1(map_rank(m_a + r * 4, c > 1 ? x : rank)));
-                    const long long pre = (long long)it.h * a.nsp * a.B * a.G + (long long)it.b * a.G + r;
-                    const long long pre_st = (long long)a.B * a.G;
-                    for (int x = 0; x < a.nsp; ++x)
-                        M = fmaxf(M, __ldcg(a.pre_ml + 2 * (pre + x * pre_st)));
-                    const float ref = M == -CUDART_INF_F ? 0.f : M;
-                    float L = 0.f;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    auto add = [&](float m_, float l_, const float4 &y) {
-                        const float f = ex2(m_ - ref);
-                        L += f * l_;
-                        acc.x += f * y.x;
-                        acc.y += f * y.y;
-                        acc.z += f * y.z;
-                        acc.w += f * y.w;
-                    };
-                    for (int x = 0; x < c; ++x) {
-                        const int rk = c > 1 ? x : rank;
-                        add(ldc1(map_rank(m_a + r * 4, rk)), ldc1(map_rank(l_a + r * 4, rk)),
-                            ldc4(map_rank(red_a + (r * EX_D + d) * 4, rk)));
+            if (parts > 1) {
+                // row r of the item is finished by block r mod parts; all loads are issued at once
+                __syncthreads();
+                cluster_sync();
+                const int r = rank + warp * parts;
+                if (r < used || MASS) {
+                    const uint32_t ra = smem_u32(red) + (r & 7) * RED * 4 + lane * 16;
+                    const uint32_t ma = smem_u32(sum_m), la = smem_u32(sum_l);
+                    float mx[8], lx[8];
+                    float4 v[8];
+                    if (r < used) {
+                        float M = -CUDART_INF_F;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            if (x >= parts) break;
+                            mx[x] = ldc1(map_rank(ma + r * 4, x));
+                            lx[x] = ldc1(map_rank(la + r * 4, x));
+                            v[x] = ldc4(map_rank(ra, x));
+                        }
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            if (x >= parts) break;
+                            M = fmaxf(M, mx[x]);
+                        }
+                        const float ref = M == -CUDART_INF_F ? 0.f : M;
+                        float L = 0.f;
+                        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            if (x >= parts) break;
+                            const float f = ex2(mx[x] - ref);
+                            L += f * lx[x];
+                            y.x += f * v[x].x;
+                            y.y += f * v[x].y;
+                            y.z += f * v[x].z;
+                            y.w += f * v[x].w;
+                        }
+                        write(r, y, L);
                     }
-#pragma unroll 4
-                    for (int x = 0; x < a.nsp; ++x) {
-                        const long long at = pre + x * pre_st;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.pre_ml + 2 * at));
-                        add(ml.x, ml.y,
-                            __ldcg(reinterpret_cast<const float4 *>(a.pre_o + at * EX_D + d)));
+                    if (MASS && warp < used) {
+                        // every block: (reference, sum) of all rows; warp = row, lane x = block x
+                        const float mr = lane < parts ? ldc1(map_rank(ma + warp * 4, lane))
+                                                      : -CUDART_INF_F;
+                        const float lr = lane < parts ? ldc1(map_rank(la + warp * 4, lane)) : 0.f;
+                        float M = mr;
+#pragma unroll
+                        for (int x = 4; x > 0; x >>= 1)
+                            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+                        const float ref = M == -CUDART_INF_F ? 0.f : M;
+                        float L = ex2(mr - ref) * lr;
+#pragma unroll
+                        for (int x = 4; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+                        if (lane == 0) {
+                            red_m[warp] = ref;
+                            red_l[warp] = L;
+                        }
                     }
-                    const float inv = inverse(L);
-                    char *op = a.out + it.b * a.o_seq + (it.h * a.G + hd) * a.o_head + tk * a.o_tok;
-                    if constexpr (F32IO)
-                        *reinterpret_cast<float4 *>(op + d * 4) =
-                            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-                    else
-                        *reinterpret_cast<uint2 *>(op + d * 2) =
-                            make_uint2(pack(acc.x * inv, acc.y * inv), pack(acc.z * inv, acc.w * inv));
                 }
-                if constexpr (MASS) {
-                    // every block of the cluster adds the weights of the rows whose scores it has
-                    float ref[EX_QROWS], inv[EX_QROWS];
-                    const float *sc[EX_QROWS];
+            }
+            if (MASS && a.by_items) {
+                // the weights of the rows whose scores this team has
+                team_sync();
+                float ref[EX_QROWS], inv[EX_QROWS];
+                const float *sc[EX_QROWS];
+#pragma unroll
+                for (int r = 0; r < EX_QROWS; ++r) {
+                    if (r >= a.G) break;
+                    ref[r] = red_m[team0 * EX_QROWS + r];
+                    inv[r] = inverse(red_l[team0 * EX_QROWS + r]);
+                    sc[r] = a.scores + (((long long)it.b * a.H + it.h) * a.G + r) * a.score_st;
+                }
+                const long long base = ((long long)it.b * a.H + it.h) * a.rows;
+                const int hi = min(it.C, w.s1 * rs);
+                // four rows per thread and turn; scores are padded to whole groups of rows
+#pragma unroll 2
+                for (int j = w.s0 * rs + 4 * (tw * 32 + lane); j < hi; j += 128 * T) {
+                    float x[4] = {0.f, 0.f, 0.f, 0.f}, old[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) old[y] = j + y < hi ? a.mass[base + j + y] : 0.f;
 #pragma unroll
                     for (int r = 0; r < EX_QROWS; ++r) {
                         if (r >= a.G) break;
-                        float M = -CUDART_INF_F, L = 0.f;
-                        for (int x = 0; x < c; ++x)
-                            M = fmaxf(M, ldc1(map_rank(m_a + r * 4, c > 1 ? x : rank)));
-                        ref[r] = M == -CUDART_INF_F ? 0.f : M;
-                        for (int x = 0; x < c; ++x)
-                            L += ex2(ldc1(map_rank(m_a + r * 4, c > 1 ? x : rank)) - ref[r]) *
-                                 ldc1(map_rank(l_a + r * 4, c > 1 ? x : rank));
-                        inv[r] = inverse(L);
-                        sc[r] = a.scores + (((long long)it.b * a.H + it.h) * a.G + r) * a.score_st;
+                        const float4 f = *reinterpret_cast<const float4 *>(sc[r] + j);
+                        x[0] += ex2(f.x - ref[r]) * inv[r];
+                        x[1] += ex2(f.y - ref[r]) * inv[r];
+                        x[2] += ex2(f.z - ref[r]) * inv[r];
+                        x[3] += ex2(f.w - ref[r]) * inv[r];
                     }
-                    const long long base = ((long long)it.b * a.H + it.h) * a.rows;
-                    const int hi = min(it.C, w.s1 * RS);
-                    for (int j = w.s0 * RS + threadIdx.x; j < hi; j += 32 * W) {
-                        float x = 0.f;
 #pragma unroll
-                        for (int r = 0; r < EX_QROWS; ++r) {
-                            if (r >= a.G) break;
-                            x += ex2(sc[r][j] - ref[r]) * inv[r];
-                        }
-                        a.mass_out[base + j] = a.mass[base + j] + x;
-                    }
+                    for (int y = 0; y < 4; ++y)
+                        if (j + y < hi) a.mass_out[base + j + y] = old[y] + x[y];
                 }
-                __syncthreads();
-                if (a.cluster > 1) cluster_sync();   // its records have been read
             }
-            have = w.next(a, rank);
+            team_sync();                             // what joined may be overwritten
+            if (parts > 1) cluster_sync();
+            have = w.next(a, rs, rank, parts);
         }
         if (late) {
             // copies still in flight end before the block does (bounded)
             atomicExch(&g_split_status, 1);
-            for (int i = max(0, ld_count - STAGES); i < ld_count; ++i)
-                wait_for(bar + (i % STAGES) * 8, (i / STAGES) & 1);
+            for (int i = max(0, loads - UNITS); i < loads; ++i)
+                wait_for(bar + (i % UNITS) * 8, (i / UNITS) & 1);
         }
     }
     // the merge waits for this kernel alone: it must not end before the one that ran beside it
@@ -774,7 +940,7 @@ exact_merge_kernel(const __grid_constant__ ExactArgs a, int rt_max, int mass_blo
     const unsigned first = ex_length(a, b, RS) + ((unsigned)h * sp.RT + rt) * sp.S;
     const int own_c0 = (int)(first / per), own_c1 = (int)((first + sp.S - 1) / per);
     const int n_own = own_c1 - own_c0 + 1;
-    if (!MASS && !a.shared_here && !a.nsp && n_own == 1) return;   // the split kernel wrote it
+    if (!MASS && !a.shared_here && n_own == 1) return;   // the split kernel wrote it
     // shared prefix: tile and row of this sequence
     int n_sh = 0, sh_c0 = 0;
     const int sh_rt = b / tpt, sh_row = (b - sh_rt * tpt) * a.G;
@@ -920,20 +1086,15 @@ cudaError_t once_per_device(std::atomic<unsigned long long> &set, const void *ke
     return e;
 }
 
-template <bool F32ROWS>
-constexpr size_t split_smem() {
-    constexpr int W = ex_warps(F32ROWS);
-    return W * STAGES * 2 * 16 * (F32ROWS ? 512 : 256) + W * EX_QROWS * (EX_D + 2) * 4 +
-           2 * EX_QROWS * 4 + W * STAGES * 8;
-}
-static_assert(split_smem<false>() <= 227 * 1024 && split_smem<true>() <= 227 * 1024, "shared memory");
+constexpr size_t SPLIT_SMEM = EX_WARPS * UNITS * (UNIT + 8) + EX_WARPS * EX_QROWS * (RED + 2) * 4 +
+                              2 * EX_QROWS * 4;
+static_assert(SPLIT_SMEM <= 227 * 1024, "shared memory");
 
-template <bool F32ROWS, bool F32IO, bool MASS>
 void config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *at, int grid, int cluster, bool after) {
     memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(32 * ex_warps(F32ROWS));
-    cfg.dynamicSmemBytes = split_smem<F32ROWS>();
+    cfg.blockDim = dim3(32 * EX_WARPS);
+    cfg.dynamicSmemBytes = SPLIT_SMEM;
     int n = 0;
     if (after) {
         at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -952,13 +1113,12 @@ void config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *at, int grid, int clus
 template <bool F32ROWS, bool F32IO, bool MASS>
 cudaError_t split(const ExactArgs &a, const ExactMaps &maps, cudaStream_t s) {
     auto kern = exact_split_kernel<F32ROWS, F32IO, MASS>;
-    const size_t bytes = split_smem<F32ROWS>();
     static std::atomic<unsigned long long> set{0};   // devices whose attribute is set
-    const cudaError_t e = once_per_device(set, reinterpret_cast<const void *>(kern), (int)bytes);
+    const cudaError_t e = once_per_device(set, reinterpret_cast<const void *>(kern), (int)SPLIT_SMEM);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute at[2];
-    config<F32ROWS, F32IO, MASS>(cfg, at, a.grid, a.cluster, a.after);
+    config(cfg, at, a.grid, a.cluster, a.after);
     cfg.stream = s;
     return cudaLaunchKernelEx(&cfg, kern, a, maps);
 }
@@ -1015,12 +1175,12 @@ int exact_split_clusters(int cluster) {
     int n = slot.load(std::memory_order_acquire);
     if (n) return n;
     auto kern = exact_split_kernel<false, true, false>;
-    if (once_per_device(set, reinterpret_cast<const void *>(kern), (int)split_smem<false>()) !=
+    if (once_per_device(set, reinterpret_cast<const void *>(kern), (int)SPLIT_SMEM) !=
         cudaSuccess)
         return 0;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute at[2];
-    config<false, true, false>(cfg, at, cluster, cluster, false);
+    config(cfg, at, cluster, cluster, false);
     if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) return 0;
     slot.store(n, std::memory_order_release);
     return n;

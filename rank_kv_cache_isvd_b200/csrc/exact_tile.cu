@@ -501,20 +501,48 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
         }
-        if (ok) {
-            const bool record = PREFIX || a.records > 1;
-            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        float *half = reinterpret_cast<float *>(ring);  // [channel][row], then m and l: free by now
+        if (ALT) {
+            // the groups' shares of the blocks join: the second leaves its part in shared memory
+            if (i == 1) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float o[32];
+                    if (mine > 0) {
+                        tmem_ld32(o_t + c * 32, o);
+                        tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        half[(c * 32 + e) * TILE_ROWS + row] = mine > 0 ? o[e] : 0.f;
+                }
+                half[TILE_ROWS * EX_D + row] = m;
+                half[TILE_ROWS * EX_D + TILE_ROWS + row] = l;
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+        }
+        if (ok && !(ALT && i == 1)) {
+            const bool record = PREFIX || a.nsp > 1;
+            float f0 = 1.f, f1 = 0.f, all_m = m, all_l = l;
+            if (ALT) {
+                const float m1 = half[TILE_ROWS * EX_D + row], l1 = half[TILE_ROWS * EX_D + TILE_ROWS + row];
+                all_m = fmaxf(m, m1);
+                const float ref = all_m == -CUDART_INF_F ? 0.f : all_m;
+                f0 = ex2(m - ref);
+                f1 = ex2(m1 - ref);
+                all_l = f0 * l + f1 * l1;
+            }
+            const float inv = all_l > 0.f ? 1.f / all_l : (all_l == 0.f ? 0.f : all_l);
             char *op = nullptr;
             float *ro = nullptr;
             if (record) {
-                const int rec = ALT ? 2 * w.sp + i : w.sp;
                 const long long at =
-                    ((long long)(w.b * a.H + w.h) * a.records + rec) * a.m * a.G +
+                    ((long long)(w.b * a.H + w.h) * a.nsp + w.sp) * a.m * a.G +
                     (long long)tok * a.G + gq;
                 ro = a.pre_o + at * EX_D;
                 if (live) {
-                    a.pre_ml[2 * at] = m;
-                    a.pre_ml[2 * at + 1] = l;
+                    a.pre_ml[2 * at] = all_m;
+                    a.pre_ml[2 * at + 1] = all_l;
                 }
             } else {
                 op = a.out + w.b * a.o_seq + (long long)(w.h * a.G + gq) * a.o_head + tok * a.o_tok;
@@ -528,6 +556,11 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                }
+                if (ALT) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = f0 * o[e] + f1 * half[(c * 32 + e) * TILE_ROWS + row];
                 }
                 if (!live) continue;
                 if (record) {
@@ -575,14 +608,14 @@ __global__ void __launch_bounds__(256) exact_tile_merge_kernel(const __grid_cons
     const long long x = row - unit * per_unit;
     const int tok = (int)(x / a.G), g = (int)(x - (long long)tok * a.G);
     if (tok >= min(max(a.q_lens ? a.q_lens[b] : a.m, 0), a.m)) return;
-    const long long at = unit * per_unit * a.records + x;
+    const long long at = unit * per_unit * a.nsp + x;
     float M = -CUDART_INF_F;
-    for (int r = 0; r < a.records; ++r) M = fmaxf(M, a.pre_ml[2 * (at + r * per_unit)]);
+    for (int r = 0; r < a.nsp; ++r) M = fmaxf(M, a.pre_ml[2 * (at + r * per_unit)]);
     const float ref = M == -CUDART_INF_F ? 0.f : M;
     float L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int r = 0; r < a.records; ++r) {
+    for (int r = 0; r < a.nsp; ++r) {
         const float2 ml = *reinterpret_cast<const float2 *>(a.pre_ml + 2 * (at + r * per_unit));
         const float f = ex2(ml.x - ref);
         const float4 v =

@@ -19,11 +19,10 @@ struct TileArgs {
     int tq;                            // tokens per tile: 128 / G
     int pairs;                         // pairs of tiles per (sequence, kv-head)
     int nsp;                           // splits of the rows' blocks
-    int records;                       // records per row: nsp, or 2 nsp where a CTA's groups split too
     char *out;                         // whole results (nsp 1) ...
     long long o_seq, o_head, o_tok;    // bytes
-    float *pre_ml, *pre_o;             // ... or records [B H][records][m G][2] and [..][128]
-                                       // (prefix: [H][records][sequences G])
+    float *pre_ml, *pre_o;             // ... or records [B H][nsp][m G][2] and [..][128]
+                                       // (prefix: [H][nsp][sequences G])
     float scale_log2;
 };
 
@@ -32,7 +31,7 @@ struct TileArgs {
 cudaError_t launch_exact_tile(const TileArgs &a, const CUtensorMap &q, const CUtensorMap &k,
                               const CUtensorMap &v, bool prefix, bool alternate, cudaStream_t s);
 
-// Joins the records of launch_exact_tile (not prefix) with nsp > 1 or alternate.
+// Joins the records of launch_exact_tile (not prefix) with nsp > 1.
 cudaError_t launch_exact_tile_merge(const TileArgs &a, cudaStream_t s);
 
 // Sticky status of the tile kernel's bounded waits on the current device: 0 or 1. Clears it.
