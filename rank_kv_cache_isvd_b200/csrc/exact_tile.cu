@@ -9,14 +9,21 @@
 //
 // One CTA of 384 threads per SM works on two tiles at once:
 // - warp 0 loads Q once and then K and V blocks by TMA into a ring of five 32 KB stages;
-// - warp 1 issues the products. S of tile i sits in tensor memory columns 128 i .. , its P (bf16)
-//   overwrites the first half of them and is the A operand of P V; O sits in columns 256 + 128 i;
+// - warp 1 issues the products. S of tile i sits in tensor memory columns 128 i .. , in two buffers
+//   of 64 keys; its P (bf16) overwrites half of its buffer and is the A operand of P V; O sits in
+//   columns 256 + 128 i;
 // - warps 4-7 and 8-11 are the softmax of tile 0 and of tile 1: a thread owns a query row, so
-//   maxima and sums need no shuffles. While one group computes, the tensor cores work for the other.
+//   maxima and sums need no shuffles.
+// With two buffers the next S is complete when a softmax step ends, and both groups compute without
+// a pause; S in one buffer of 128 keys had to wait for P V, 1.4 us of every 2.4 us.
+//
+// A prefix with no more rows than one tile is bound by HBM instead. There the two groups share the
+// tile and take alternate blocks (S of 128 keys, one buffer), which keeps fewer stages of the ring in
+// use and more in flight; their results join in shared memory at the end.
 //
 // m moves only when a row's maximum passes it by 2^8 (a power of two that P, O and l carry along
 // exactly enough: P is at most 256). Moving it rescales O in tensor memory, which the softmax warp
-// does itself: S of this block being complete says that the P V before it is too.
+// does itself once the P V before it is complete.
 //
 // P is rounded to bf16 (half a step, 2^-9 of the leading bits' scale, at random over the keys);
 // the sum l takes the unrounded values, and all sums are float32.
@@ -48,7 +55,7 @@ static_assert(128 * REG_LO + 256 * REG_HI <= TT * REG_LAUNCH, "register split");
 __device__ int g_tile_status;
 
 struct Bars {
-    uint64_t q_full, kv_full[NSTAGE], kv_empty[NSTAGE], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full, kv_full[NSTAGE], kv_empty[NSTAGE], s_full[2][2], p_full[2][2], pv_done[2], o_full;
     uint32_t tmem;
     int abort, issued;
 };
@@ -91,31 +98,56 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, i
         "r"(smem_u32(bar))
         : "memory");
 }
-// D[tmem] (+)= A[smem] B[smem]^T and D[tmem] (+)= A[tmem] B[smem]^T, bf16 operands.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The instructions of the issuing warp run with all its lanes in step, and `lead` (1 in one lane, 0 in
+// the others) is their predicate: operands then stay in uniform registers. Issued under a branch on
+// the lane, each product took about 100 cycles to issue, against the 50 to 65 that it runs.
+//
+// D[tmem] (+)= A[smem] B[smem]^T and D[tmem] (+)= A[tmem] B[smem]^T, bf16 operands. Shared-memory
+// descriptors are given by their low words and the high one.
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b,
+                                       uint32_t hi, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tmov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc), "r"(lead)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b,
+                                       uint32_t hi, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc), "r"(lead)
         : "memory");
 }
-// Descriptor of an operand whose M or N index is contiguous (V: channels), 128-byte swizzle: 64
-// channels x 8 rows per 1024 bytes, the next 8 rows 1024 bytes on, the next 64 channels one half on.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(HALF_BYTES >> 4) << 16 |
-           (uint64_t)(1024u >> 4) << 32 | (uint64_t)1u << 46 | (uint64_t)2u << 61;
+// Arrives on the barrier when every product issued before is complete.
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(lead)
+        : "memory");
 }
-// D fp32, A and B bf16, 128 x 128; b_mn: B's N index is contiguous.
-__host__ __device__ constexpr uint32_t idesc_tile(bool b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((128u >> 3) << 17) |
-           ((128u >> 4) << 24);
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+// High words: 8 rows of 128 bytes per 1024, 128-byte swizzle. K-major (Q, K: channels contiguous),
+// and operands whose N index is contiguous (V: channels), where the low word's upper half is the
+// distance of the next 64 channels.
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t addr) {
+    return ((addr & 0x3FFFFu) >> 4) | (uint32_t)(HALF_BYTES >> 4) << 16;
+}
+// D fp32, A and B bf16, 128 x n; b_mn: B's N index is contiguous.
+__host__ __device__ constexpr uint32_t idesc_tile(bool b_mn, int n) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
@@ -223,7 +255,8 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
     uint8_t *qs = smem, *ring = smem + 2 * BLOCK_BYTES;
     Bars *bars = reinterpret_cast<Bars *>(ring + NSTAGE * BLOCK_BYTES);
     volatile int *abort_flag = &bars->abort;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);     // the same in all lanes
     const Work w = work_of<PREFIX>(a, ALT);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (w.t0 >= w.ql) return;
@@ -235,10 +268,13 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
             mbar_init(&bars->kv_full[i], 1);
             mbar_init(&bars->kv_empty[i], 1);
         }
+        mbar_init(&bars->o_full, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars->s_full[i], 1);
-            mbar_init(&bars->p_full[i], 4);
-            mbar_init(&bars->o_full[i], 1);
+            for (int x = 0; x < 2; ++x) {
+                mbar_init(&bars->s_full[i][x], 1);
+                mbar_init(&bars->p_full[i][x], 4);
+            }
+            mbar_init(&bars->pv_done[i], 1);
         }
         bars->abort = bars->issued = 0;
         fence_mbar_init();
@@ -253,6 +289,7 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
     // take them: both tiles on every block: K0 V0 K1 V1 ...; the two groups on alternate blocks of
     // one tile: K0 K1 V0 K2 V1 K3 ...
     constexpr int AHEAD = ALT ? 2 : 1;
+    constexpr int KC = ALT ? 128 : 64;             // keys per step of a tile
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LO));
       if (warp == 0) {
@@ -289,30 +326,40 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
             bars->issued = issued;
         }
       } else if (warp == 1) {
-        int use = 0;                                   // blocks taken from the ring
+        const uint32_t lead = elect_one();
+        const uint32_t ring_a = smem_u32(ring), empty_a = smem_u32(bars->kv_empty);
+        const uint32_t q_desc = desc_k(smem_u32(qs));
+        int st = 0;                                    // stage of the ring to take next
+        uint32_t phase = 0;
         auto wait = [&](uint64_t *bar, uint32_t parity) {   // the same answer in every lane
             return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag)) != 0;
         };
-        auto full = [&]() {
-            return wait(&bars->kv_full[use % NSTAGE], (use / NSTAGE) & 1);
+        auto full = [&]() { return wait(&bars->kv_full[st], phase); };
+        auto full_next = [&]() {
+            return st + 1 < NSTAGE ? wait(&bars->kv_full[st + 1], phase)
+                                   : wait(&bars->kv_full[0], phase ^ 1);
         };
-        auto stage_addr = [&]() { return smem_u32(ring + (use % NSTAGE) * BLOCK_BYTES); };
-        auto qk = [&](int i) {                          // S_i = Q_i K^T
-            const uint32_t q = smem_u32(qs + (ALT ? 0 : i) * BLOCK_BYTES), k = stage_addr();
+        auto next_addr = [&]() { return ring_a + (st + 1 < NSTAGE ? st + 1 : 0) * BLOCK_BYTES; };
+        // S_i = Q_i K^T for KC keys from `h` KC on, into buffer `buf`
+        auto qk = [&](int i, int h, int buf, uint32_t k) {
+            const uint32_t q = q_desc + ((ALT ? 0 : i) * BLOCK_BYTES >> 4);
+            const uint32_t kd = desc_k(k) + (h * KC * 128 >> 4);
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
-                const uint32_t off = (s >> 2) * HALF_BYTES + (s & 3) * 32;
-                mma_ss(tmem + i * 128, sw128_kmajor_desc(q + off), sw128_kmajor_desc(k + off),
-                       idesc_tile(false), s > 0);
+                const uint32_t off = ((s >> 2) * HALF_BYTES + (s & 3) * 32) >> 4;
+                mma_ss(lead, tmem + i * 128 + buf * KC, q + off, kd + off, DESC_HI,
+                       idesc_tile(false, KC), s > 0);
             }
-            mma_commit(&bars->s_full[i]);
+            commit(lead, smem_u32(&bars->s_full[i][buf]));
         };
-        auto pv = [&](int i, bool acc) {                // O_i (+)= P_i V
-            const uint32_t v = stage_addr();
+        // O_i (+)= P_i V for them
+        auto pv = [&](int i, int h, int buf, uint32_t v, bool acc) {
+            const uint32_t vd = desc_mn(v) + (h * KC * 128 >> 4);
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
-                mma_ts(tmem + 256 + i * 128, tmem + i * 128 + s * 8, sw128_mnmajor_desc(v + s * 2048),
-                       idesc_tile(true), acc || s > 0);
+            for (int s = 0; s < KC / 16; ++s)
+                mma_ts(lead, tmem + 256 + i * 128, tmem + i * 128 + buf * KC + s * 8,
+                       vd + (s * 2048 >> 4), DESC_HI, idesc_tile(true, 128), acc || s > 0);
+            if (!ALT) commit(lead, smem_u32(&bars->pv_done[i]));
         };
         // Values of rows that no token of the pair sees may be anything: 0 x NaN would reach O.
         auto scrub = [&](int blk) {
@@ -321,7 +368,7 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
             const bool tail = base + TILE_ROWS - 1 > w.p1;
             const bool gap = base <= w.p0 - a.window && base + TILE_ROWS > a.sinks;
             if (!tail && !gap) return;
-            uint8_t *v = ring + (use % NSTAGE) * BLOCK_BYTES;
+            uint8_t *v = ring + st * BLOCK_BYTES;
             for (int r = lane; r < TILE_ROWS; r += 32) {
                 const int j = base + r;
                 if (j <= w.p1 && (j < a.sinks || j > w.p0 - a.window)) continue;
@@ -333,74 +380,80 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
             __syncwarp();
         };
         auto release = [&]() {
-            if (lane == 0) mma_commit(&bars->kv_empty[use % NSTAGE]);
-            ++use;
+            commit(lead, empty_a + st * 8);
+            if (++st == NSTAGE) {
+                st = 0;
+                phase ^= 1;
+            }
         };
+        auto addr = [&]() { return ring_a + st * BLOCK_BYTES; };
         bool ok = N > 0 && wait(&bars->q_full, 0);
         if (!ALT) {
             if (ok) ok = full();
             if (ok) {
-                if (lane == 0) {
-                    qk(0);
-                    qk(1);
-                }
+                qk(0, 0, 0, addr());
+                qk(1, 0, 0, addr());
+                qk(0, 1, 1, addr());
+                qk(1, 1, 1, addr());
                 release();
             }
             for (int j = 0; ok && j < N; ++j) {
-                ok = full();                            // V_j
-                if (ok) scrub(j);
-                if (ok) ok = wait(&bars->p_full[0], j & 1);
+                ok = full();                            // V_j; K_j+1 is behind it
                 if (!ok) break;
-                tc_fence_after();
-                if (lane == 0) pv(0, j > 0);
-                const int v_use = use;
-                if (j + 1 < N) {
-                    ++use;
-                    ok = full();                        // K_j+1
-                    if (!ok) break;
-                    if (lane == 0) qk(0);
-                    use = v_use;
+                scrub(j);
+                const bool more = j + 1 < N;
+                const uint32_t v = addr(), k = next_addr();
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int h = u >> 1, i = u & 1;
+                    if (ok) ok = wait(&bars->p_full[i][h], j & 1);
+                    if (ok) {
+                        tc_fence_after();
+                        pv(i, h, h, v, j + h > 0);
+                        if (u == 0 && more) ok = full_next();
+                        if (ok && more) qk(i, h, h, k);
+                    }
                 }
-                ok = wait(&bars->p_full[1], j & 1);
                 if (!ok) break;
-                tc_fence_after();
-                if (lane == 0) pv(1, j > 0);
                 release();
-                if (j + 1 < N) {
-                    if (lane == 0) qk(1);
-                    release();
-                }
+                if (more) release();
             }
         } else {
-            for (int i = 0; ok && i < 2 && i < N; ++i) {
-                ok = full();
-                if (!ok) break;
-                if (lane == 0) qk(i);
-                release();
-            }
-            for (int j = 0; ok && j < N; ++j) {
-                const int i = j & 1;
-                ok = full();
-                if (ok) scrub(j);
-                if (ok) ok = wait(&bars->p_full[i], (j >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                if (lane == 0) pv(i, j > 1);
-                release();
-                if (j + 2 < N) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (ok && i < N) {
                     ok = full();
-                    if (!ok) break;
-                    if (lane == 0) qk(i);
+                    if (ok) {
+                        qk(i, 0, 0, addr());
+                        release();
+                    }
+                }
+            }
+            for (int j0 = 0; ok && j0 < N; j0 += 2) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = j0 + i;
+                    if (!ok || j >= N) continue;
+                    ok = full();
+                    if (ok) scrub(j);
+                    if (ok) ok = wait(&bars->p_full[i][0], (j >> 1) & 1);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    pv(i, 0, 0, addr(), j > 1);
                     release();
+                    if (j + 2 < N) {
+                        ok = full();
+                        if (ok) {
+                            qk(i, 0, 0, addr());
+                            release();
+                        }
+                    }
                 }
             }
         }
         // commits follow all products before them, so these come when both tiles are complete;
         // after an abort they bound what is in flight
-        if (lane == 0 && N > 0) {
-            mma_commit(&bars->o_full[0]);
-            mma_commit(&bars->o_full[1]);
-        }
+        if (N > 0) commit(lead, smem_u32(&bars->o_full));
       }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_HI));
@@ -416,43 +469,43 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
         const int tile0 = w.t0 + (ALT ? 0 : i * a.tq);
         const int tp0 = PREFIX ? w.n - 1 : w.n - w.ql + tile0;
         const int tp1 = PREFIX ? w.n - 1 : w.n - w.ql + min(tile0 + a.tq, w.ql) - 1;
-        const int mine = ALT ? (N - i + 1) / 2 : N;
+        const int mine = ALT ? (N - i + 1) / 2 : 2 * N;   // steps of KC keys
+        constexpr int CH = KC / 32;
         float m = -CUDART_INF_F;
         float2 l2 = make_float2(0.f, 0.f);
         bool ok = true;
         for (int x = 0; x < mine; ++x) {
-            ok = wait_bar(&bars->s_full[i], x & 1, abort_flag);
+            const int buf = ALT ? 0 : x & 1;
+            ok = wait_bar(&bars->s_full[i][buf], (ALT ? x : x >> 1) & 1, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            float s[4][32];
+            const uint32_t s_x = s_t + buf * KC;
+            float s[CH][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(s_t + c * 32, s[c]);
+            for (int c = 0; c < CH; ++c) tmem_ld32(s_x + c * 32, s[c]);
             tmem_wait_ld();
-            const int base = w.base(ALT ? 2 * x + i : x);
-            const bool inside = PREFIX ? base + TILE_ROWS <= w.n
-                                       : base + TILE_ROWS - 1 <= tp0 &&
-                                             (base + TILE_ROWS <= a.sinks || base > tp1 - a.window);
+            const int base = ALT ? w.base(2 * x + i) : w.base(x >> 1) + buf * KC;
+            const bool inside = PREFIX ? base + KC <= w.n
+                                       : base + KC - 1 <= tp0 &&
+                                             (base + KC <= a.sinks || base > tp1 - a.window);
             if (!inside) {
                 const int hi = pos - base, lo = PREFIX ? 0 : pos - a.window + 1 - base;
                 const int sk = PREFIX ? 0 : a.sinks - base;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < CH; ++c)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         const int j = c * 32 + e;
                         if (!(j <= hi && (j >= lo || j < sk))) s[c][e] = -CUDART_INF_F;
                     }
             }
-            float t0 = s[0][0], t1 = s[1][0], t2 = s[2][0], t3 = s[3][0];
+            float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-            for (int e = 1; e < 32; ++e) {
-                t0 = fmaxf(t0, s[0][e]);
-                t1 = fmaxf(t1, s[1][e]);
-                t2 = fmaxf(t2, s[2][e]);
-                t3 = fmaxf(t3, s[3][e]);
-            }
-            const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * a.scale_log2;
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) tops[e & 3] = fmaxf(tops[e & 3], s[c][e]);
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale_log2;
             const bool raise = top > m + 8.f || (m == -CUDART_INF_F && top > m);
             if (__any_sync(0xffffffffu, raise)) {
                 const float nm = raise ? top : m;
@@ -461,6 +514,13 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
                 l2.x *= f;
                 l2.y *= f;
                 if (x > 0) {
+                    if (!ALT) {
+                        // S of this step was issued before the last P V, which O has to have
+                        ok = wait_bar(&bars->pv_done[i], (x - 1) & 1, abort_flag);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         float o[32];
@@ -475,9 +535,9 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
             }
             const float ref = m == -CUDART_INF_F ? 0.f : m;
             const float2 sc = make_float2(a.scale_log2, a.scale_log2), nr = make_float2(-ref, -ref);
+            uint32_t p[KC / 64][32];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t p[32];
+            for (int c = 0; c < KC / 64; ++c) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
                     const int q = c * 64 + 2 * e;
@@ -485,19 +545,19 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
                     y.x = ex2(y.x);
                     y.y = ex2(y.y);
                     l2 = add2(l2, y);
-                    p[e] = pack(y.x, y.y);
+                    p[c][e] = pack(y.x, y.y);
                 }
-                tmem_st32(s_t + c * 32, p);
+                tmem_st32(s_x + c * 32, p[c]);
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive(&bars->p_full[i]);
+            if (lane == 0) arrive(&bars->p_full[i][buf]);
         }
         // ---- the tile is complete: out = O / l, or a record of this split -----------------------
         const float l = l2.x + l2.y;
         if (N > 0 && ok) {
-            ok = wait_bar(&bars->o_full[i], 0, abort_flag);
+            ok = wait_bar(&bars->o_full, 0, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
         }
@@ -584,7 +644,7 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
         // products and copies in flight end before the block does (bounded waits)
         atomicExch(&g_tile_status, 1);
         if (N > 0) {
-            bool late = !mbar_wait(&bars->o_full[1], 0) | !mbar_wait(&bars->q_full, 0);
+            bool late = !mbar_wait(&bars->o_full, 0) | !mbar_wait(&bars->q_full, 0);
             for (int i = max(0, bars->issued - NSTAGE); i < bars->issued; ++i)
                 late |= !mbar_wait(&bars->kv_full[i % NSTAGE], (i / NSTAGE) & 1);
             (void)late;
