@@ -9,21 +9,21 @@
 //
 // One CTA of 384 threads per SM works on two tiles at once:
 // - warp 0 loads Q once and then K and V blocks by TMA into a ring of five 32 KB stages;
-// - warp 1 issues the products. S of tile i sits in tensor memory columns 128 i .. , in two buffers
-//   of 64 keys; its P (bf16) overwrites half of its buffer and is the A operand of P V; O sits in
-//   columns 256 + 128 i;
+// - warp 1 issues the products. S of tile i sits in tensor memory columns 128 i .. , its P (bf16)
+//   overwrites the first half of them and is the A operand of P V; O sits in columns 256 + 128 i;
 // - warps 4-7 and 8-11 are the softmax of tile 0 and of tile 1: a thread owns a query row, so
-//   maxima and sums need no shuffles.
-// With two buffers the next S is complete when a softmax step ends, and both groups compute without
-// a pause; S in one buffer of 128 keys had to wait for P V, 1.4 us of every 2.4 us.
+//   maxima and sums need no shuffles. While one group computes, the tensor cores work for the other;
+//   P V of the first 64 keys of a block runs while the weights of the others are computed.
+// (S in two buffers of 64 keys, so that the next S is complete when a softmax ends, was slower: with
+// 64 columns the products read Q from shared memory at its full rate and take 50 cycles for the work
+// of 32, and the tensor cores become the bound.)
 //
 // A prefix with no more rows than one tile is bound by HBM instead. There the two groups share the
-// tile and take alternate blocks (S of 128 keys, one buffer), which keeps fewer stages of the ring in
-// use and more in flight; their results join in shared memory at the end.
+// tile and take alternate blocks; their results join in shared memory at the end.
 //
 // m moves only when a row's maximum passes it by 2^8 (a power of two that P, O and l carry along
 // exactly enough: P is at most 256). Moving it rescales O in tensor memory, which the softmax warp
-// does itself once the P V before it is complete.
+// does itself: S of this block being complete says that the P V before it is too.
 //
 // P is rounded to bf16 (half a step, 2^-9 of the leading bits' scale, at random over the keys);
 // the sum l takes the unrounded values, and all sums are float32.
@@ -55,7 +55,7 @@ static_assert(128 * REG_LO + 256 * REG_HI <= TT * REG_LAUNCH, "register split");
 __device__ int g_tile_status;
 
 struct Bars {
-    uint64_t q_full, kv_full[NSTAGE], kv_empty[NSTAGE], s_full[2][2], p_full[2][2], pv_done[2], o_full;
+    uint64_t q_full, kv_full[NSTAGE], kv_empty[NSTAGE], s_full[2], p_full[2][2], o_full;
     uint32_t tmem;
     int abort, issued;
 };
@@ -144,10 +144,10 @@ __device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return ((addr & 0x3F
 __device__ __forceinline__ uint32_t desc_mn(uint32_t addr) {
     return ((addr & 0x3FFFFu) >> 4) | (uint32_t)(HALF_BYTES >> 4) << 16;
 }
-// D fp32, A and B bf16, 128 x n; b_mn: B's N index is contiguous.
-__host__ __device__ constexpr uint32_t idesc_tile(bool b_mn, int n) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) |
-           ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+// D fp32, A and B bf16, 128 x 128; b_mn: B's N index is contiguous.
+__host__ __device__ constexpr uint32_t idesc_tile(bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((128u >> 3) << 17) |
+           ((128u >> 4) << 24);
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
@@ -270,11 +270,9 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
         }
         mbar_init(&bars->o_full, 1);
         for (int i = 0; i < 2; ++i) {
-            for (int x = 0; x < 2; ++x) {
-                mbar_init(&bars->s_full[i][x], 1);
-                mbar_init(&bars->p_full[i][x], 4);
-            }
-            mbar_init(&bars->pv_done[i], 1);
+            mbar_init(&bars->s_full[i], 1);
+            mbar_init(&bars->p_full[i][0], 4);
+            mbar_init(&bars->p_full[i][1], 4);
         }
         bars->abort = bars->issued = 0;
         fence_mbar_init();
@@ -289,7 +287,6 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
     // take them: both tiles on every block: K0 V0 K1 V1 ...; the two groups on alternate blocks of
     // one tile: K0 K1 V0 K2 V1 K3 ...
     constexpr int AHEAD = ALT ? 2 : 1;
-    constexpr int KC = ALT ? 128 : 64;             // keys per step of a tile
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LO));
       if (warp == 0) {
@@ -335,31 +332,30 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
             return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag)) != 0;
         };
         auto full = [&]() { return wait(&bars->kv_full[st], phase); };
-        auto full_next = [&]() {
-            return st + 1 < NSTAGE ? wait(&bars->kv_full[st + 1], phase)
-                                   : wait(&bars->kv_full[0], phase ^ 1);
-        };
-        auto next_addr = [&]() { return ring_a + (st + 1 < NSTAGE ? st + 1 : 0) * BLOCK_BYTES; };
-        // S_i = Q_i K^T for KC keys from `h` KC on, into buffer `buf`
-        auto qk = [&](int i, int h, int buf, uint32_t k) {
-            const uint32_t q = q_desc + ((ALT ? 0 : i) * BLOCK_BYTES >> 4);
-            const uint32_t kd = desc_k(k) + (h * KC * 128 >> 4);
+        auto qk = [&](int i, uint32_t k) {              // S_i = Q_i K^T
+            const uint32_t q = q_desc + ((ALT ? 0 : i) * BLOCK_BYTES >> 4), kd = desc_k(k);
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
                 const uint32_t off = ((s >> 2) * HALF_BYTES + (s & 3) * 32) >> 4;
-                mma_ss(lead, tmem + i * 128 + buf * KC, q + off, kd + off, DESC_HI,
-                       idesc_tile(false, KC), s > 0);
+                mma_ss(lead, tmem + i * 128, q + off, kd + off, DESC_HI, idesc_tile(false), s > 0);
             }
-            commit(lead, smem_u32(&bars->s_full[i][buf]));
+            commit(lead, smem_u32(&bars->s_full[i]));
         };
-        // O_i (+)= P_i V for them
-        auto pv = [&](int i, int h, int buf, uint32_t v, bool acc) {
-            const uint32_t vd = desc_mn(v) + (h * KC * 128 >> 4);
+        // O_i (+)= P_i V, 64 keys at a time: the first while the second's weights are computed
+        auto pv = [&](int i, uint32_t v, uint32_t parity, bool acc) {
+            const uint32_t vd = desc_mn(v);
+            bool ok = true;
 #pragma unroll
-            for (int s = 0; s < KC / 16; ++s)
-                mma_ts(lead, tmem + 256 + i * 128, tmem + i * 128 + buf * KC + s * 8,
-                       vd + (s * 2048 >> 4), DESC_HI, idesc_tile(true, 128), acc || s > 0);
-            if (!ALT) commit(lead, smem_u32(&bars->pv_done[i]));
+            for (int h = 0; h < 2; ++h) {
+                if (ok) ok = wait(&bars->p_full[i][h], parity);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int s = 4 * h; s < 4 * h + 4; ++s)
+                    mma_ts(lead, tmem + 256 + i * 128, tmem + i * 128 + s * 8, vd + (s * 2048 >> 4),
+                           DESC_HI, idesc_tile(true), acc || s > 0);
+            }
+            return ok;
         };
         // Values of rows that no token of the pair sees may be anything: 0 x NaN would reach O.
         auto scrub = [&](int blk) {
@@ -391,10 +387,8 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
         if (!ALT) {
             if (ok) ok = full();
             if (ok) {
-                qk(0, 0, 0, addr());
-                qk(1, 0, 0, addr());
-                qk(0, 1, 1, addr());
-                qk(1, 1, 1, addr());
+                qk(0, addr());
+                qk(1, addr());
                 release();
             }
             for (int j = 0; ok && j < N; ++j) {
@@ -402,21 +396,20 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
                 if (!ok) break;
                 scrub(j);
                 const bool more = j + 1 < N;
-                const uint32_t v = addr(), k = next_addr();
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int h = u >> 1, i = u & 1;
-                    if (ok) ok = wait(&bars->p_full[i][h], j & 1);
-                    if (ok) {
-                        tc_fence_after();
-                        pv(i, h, h, v, j + h > 0);
-                        if (u == 0 && more) ok = full_next();
-                        if (ok && more) qk(i, h, h, k);
-                    }
+                const uint32_t v = addr(), k = ring_a + (st + 1 < NSTAGE ? st + 1 : 0) * BLOCK_BYTES;
+                ok = pv(0, v, j & 1, j > 0);
+                if (ok && more) {
+                    ok = st + 1 < NSTAGE ? wait(&bars->kv_full[st + 1], phase)
+                                         : wait(&bars->kv_full[0], phase ^ 1);
+                    if (ok) qk(0, k);
                 }
+                if (ok) ok = pv(1, v, j & 1, j > 0);
                 if (!ok) break;
                 release();
-                if (more) release();
+                if (more) {
+                    qk(1, k);
+                    release();
+                }
             }
         } else {
 #pragma unroll
@@ -424,7 +417,7 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
                 if (ok && i < N) {
                     ok = full();
                     if (ok) {
-                        qk(i, 0, 0, addr());
+                        qk(i, addr());
                         release();
                     }
                 }
@@ -436,15 +429,13 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
                     if (!ok || j >= N) continue;
                     ok = full();
                     if (ok) scrub(j);
-                    if (ok) ok = wait(&bars->p_full[i][0], (j >> 1) & 1);
+                    if (ok) ok = pv(i, addr(), (j >> 1) & 1, j > 1);
                     if (!ok) continue;
-                    tc_fence_after();
-                    pv(i, 0, 0, addr(), j > 1);
                     release();
                     if (j + 2 < N) {
                         ok = full();
                         if (ok) {
-                            qk(i, 0, 0, addr());
+                            qk(i, addr());
                             release();
                         }
                     }
@@ -469,31 +460,28 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
         const int tile0 = w.t0 + (ALT ? 0 : i * a.tq);
         const int tp0 = PREFIX ? w.n - 1 : w.n - w.ql + tile0;
         const int tp1 = PREFIX ? w.n - 1 : w.n - w.ql + min(tile0 + a.tq, w.ql) - 1;
-        const int mine = ALT ? (N - i + 1) / 2 : 2 * N;   // steps of KC keys
-        constexpr int CH = KC / 32;
+        const int mine = ALT ? (N - i + 1) / 2 : N;
         float m = -CUDART_INF_F;
         float2 l2 = make_float2(0.f, 0.f);
         bool ok = true;
         for (int x = 0; x < mine; ++x) {
-            const int buf = ALT ? 0 : x & 1;
-            ok = wait_bar(&bars->s_full[i][buf], (ALT ? x : x >> 1) & 1, abort_flag);
+            ok = wait_bar(&bars->s_full[i], x & 1, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t s_x = s_t + buf * KC;
-            float s[CH][32];
+            float s[4][32];
 #pragma unroll
-            for (int c = 0; c < CH; ++c) tmem_ld32(s_x + c * 32, s[c]);
+            for (int c = 0; c < 4; ++c) tmem_ld32(s_t + c * 32, s[c]);
             tmem_wait_ld();
-            const int base = ALT ? w.base(2 * x + i) : w.base(x >> 1) + buf * KC;
-            const bool inside = PREFIX ? base + KC <= w.n
-                                       : base + KC - 1 <= tp0 &&
-                                             (base + KC <= a.sinks || base > tp1 - a.window);
+            const int base = w.base(ALT ? 2 * x + i : x);
+            const bool inside = PREFIX ? base + TILE_ROWS <= w.n
+                                       : base + TILE_ROWS - 1 <= tp0 &&
+                                             (base + TILE_ROWS <= a.sinks || base > tp1 - a.window);
             if (!inside) {
                 const int hi = pos - base, lo = PREFIX ? 0 : pos - a.window + 1 - base;
                 const int sk = PREFIX ? 0 : a.sinks - base;
 #pragma unroll
-                for (int c = 0; c < CH; ++c)
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         const int j = c * 32 + e;
@@ -502,9 +490,9 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
             }
             float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-            for (int c = 0; c < CH; ++c)
+            for (int e = 0; e < 32; ++e)
 #pragma unroll
-                for (int e = 0; e < 32; ++e) tops[e & 3] = fmaxf(tops[e & 3], s[c][e]);
+                for (int c = 0; c < 4; ++c) tops[c] = fmaxf(tops[c], s[c][e]);
             const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale_log2;
             const bool raise = top > m + 8.f || (m == -CUDART_INF_F && top > m);
             if (__any_sync(0xffffffffu, raise)) {
@@ -514,13 +502,7 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
                 l2.x *= f;
                 l2.y *= f;
                 if (x > 0) {
-                    if (!ALT) {
-                        // S of this step was issued before the last P V, which O has to have
-                        ok = wait_bar(&bars->pv_done[i], (x - 1) & 1, abort_flag);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                        tc_fence_after();
-                    }
+                    // S of this block was issued behind the P V before it: O has that
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         float o[32];
@@ -535,9 +517,9 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
             }
             const float ref = m == -CUDART_INF_F ? 0.f : m;
             const float2 sc = make_float2(a.scale_log2, a.scale_log2), nr = make_float2(-ref, -ref);
-            uint32_t p[KC / 64][32];
 #pragma unroll
-            for (int c = 0; c < KC / 64; ++c) {
+            for (int c = 0; c < 2; ++c) {
+                uint32_t p[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
                     const int q = c * 64 + 2 * e;
@@ -545,14 +527,14 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
                     y.x = ex2(y.x);
                     y.y = ex2(y.y);
                     l2 = add2(l2, y);
-                    p[c][e] = pack(y.x, y.y);
+                    p[e] = pack(y.x, y.y);
                 }
-                tmem_st32(s_x + c * 32, p[c]);
+                tmem_st32(s_t + c * 32, p);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(&bars->p_full[i][c]);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive(&bars->p_full[i][buf]);
         }
         // ---- the tile is complete: out = O / l, or a record of this split -----------------------
         const float l = l2.x + l2.y;
@@ -593,20 +575,18 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
                 all_l = f0 * l + f1 * l1;
             }
             const float inv = all_l > 0.f ? 1.f / all_l : (all_l == 0.f ? 0.f : all_l);
-            char *op = nullptr;
-            float *ro = nullptr;
-            if (record) {
-                const long long at =
-                    ((long long)(w.b * a.H + w.h) * a.nsp + w.sp) * a.m * a.G +
-                    (long long)tok * a.G + gq;
-                ro = a.pre_o + at * EX_D;
-                if (live) {
-                    a.pre_ml[2 * at] = all_m;
-                    a.pre_ml[2 * at + 1] = all_l;
-                }
-            } else {
-                op = a.out + w.b * a.o_seq + (long long)(w.h * a.G + gq) * a.o_head + tok * a.o_tok;
-            }
+            // Rows leave through shared memory (free by now), so that a warp's stores are contiguous:
+            // a lane owns a row here and writes 16-byte pieces of two (bf16) or one (record) there.
+            const long long at = ((long long)(w.b * a.H + w.h) * a.nsp + w.sp) * a.m * a.G +
+                                 (long long)tok * a.G + gq;
+            char *to = record ? reinterpret_cast<char *>(a.pre_o + at * EX_D)
+                              : a.out + w.b * a.o_seq + (long long)(w.h * a.G + gq) * a.o_head +
+                                    tok * a.o_tok;
+            if (!live) to = nullptr;
+            else if (record)
+                *reinterpret_cast<float2 *>(a.pre_ml + 2 * at) = make_float2(all_m, all_l);
+            uint8_t *stage = ring + (ALT ? 3 * BLOCK_BYTES : 0) + (ALT ? warp & 3 : warp - 4) * 8192;
+            // two halves of 64 channels (record: four of 32), 128 bytes of a row each
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 float o[32];
@@ -622,19 +602,34 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
                     for (int e = 0; e < 32; ++e)
                         o[e] = f0 * o[e] + f1 * half[(c * 32 + e) * TILE_ROWS + row];
                 }
-                if (!live) continue;
                 if (record) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4 *>(ro + c * 32 + e) =
-                            make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<float4 *>(stage + lane * 128 + ((e ^ (lane & 7)) * 16)) =
+                            make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4 *>(op + (c * 32 + e) * 2) = make_uint4(
-                            pack(o[e] * inv, o[e + 1] * inv), pack(o[e + 2] * inv, o[e + 3] * inv),
-                            pack(o[e + 4] * inv, o[e + 5] * inv), pack(o[e + 6] * inv, o[e + 7] * inv));
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4 *>(stage + lane * 128 +
+                                                   (((4 * (c & 1) + e) ^ (lane & 7)) * 16)) =
+                            make_uint4(pack(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                       pack(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                       pack(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                       pack(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                    if (!(c & 1)) continue;
                 }
+                __syncwarp();
+                const int part = record ? c : c >> 1;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {        // four rows at a time, 128 bytes each
+                    const int r = 4 * k + (lane >> 3), e = lane & 7;
+                    char *dst = reinterpret_cast<char *>(
+                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), r));
+                    const uint4 v =
+                        *reinterpret_cast<const uint4 *>(stage + r * 128 + ((e ^ (r & 7)) * 16));
+                    if (dst) *reinterpret_cast<uint4 *>(dst + part * 128 + e * 16) = v;
+                }
+                __syncwarp();
             }
         }
         tc_fence_before();
