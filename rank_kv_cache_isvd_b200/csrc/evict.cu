@@ -6,12 +6,13 @@
 // slots below R, both in ascending order: sources and targets are disjoint, so the rows move in
 // place without an order between them, and only what has to move is touched.
 //
-// evict_select_kernel: one block per unit, keys in registers up to 32768 rows. T, the R-th largest
+// evict_select_kernel: a block, or a cluster of them, per unit, keys in registers. T, the R-th largest
 // key, comes from three digits of 11, 11 and 10 bits: a histogram of the keys that share the digits
 // found so far, and the digit where the count from above reaches R. 11 bits are sign, exponent and
 // two bits of the fraction, so that weights of a few octaves spread over enough bins for the
-// shared-memory atomics (they took 32 counting passes' place, 20 us of 85 us at 32768 rows). The
+// shared-memory atomics. (32 counting passes, one per bit, took twice the time at 32768 rows.) The
 // number of kept rows before a slot then gives every freed slot and every moved row its index.
+// Blocks behind the units' copy what the slots below R have into the output arrays meanwhile.
 //
 // evict_move_kernel copies the rows, which is what the operator is bound by (HBM: 4 x 256 bytes per
 // moved bf16 row).
@@ -27,6 +28,19 @@ constexpr int BINS = 2048;
 constexpr int MOVE_T = 256;
 constexpr int MOVE_ROWS = 4;               // 16-byte pieces in flight per thread
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+// The value at this block's shared address of `p`, in the cluster's block `rank`.
+__device__ __forceinline__ unsigned of_rank(const void *p, int rank) {
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
+    unsigned v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(r) : "memory");
+    return v;
+}
+
 // Order-preserving key of a weight (-0 equals 0; a NaN, of either sign, is above all weights);
 // fixed rows get the largest.
 __device__ __forceinline__ uint32_t evict_key(float w, int pos, int sinks, int latest) {
@@ -39,174 +53,247 @@ __device__ __forceinline__ uint32_t evict_key(float w, int pos, int sinks, int l
 // E keys per thread and turn: a turn is SEL_T * E slots, of which each warp has a run, in order:
 // slot = turn + warp 32 E + 32 e + lane. With one turn the keys stay in registers.
 template <int E>
-__global__ void __launch_bounds__(SEL_T, 1) evict_select_kernel(EvictArgs a) {
-    __shared__ unsigned hist[BINS];
-    __shared__ int sh[SEL_W], sh2[SEL_W];
+__global__ void __launch_bounds__(SEL_T, 1) evict_select_kernel(EvictArgs a, int cluster) {
+    __shared__ unsigned hist[2][BINS];
+    __shared__ unsigned sh[SEL_W], sh2[SEL_W];
     __shared__ unsigned found[2];                    // digit, keys above it
-    __shared__ int kept_low;                         // kept rows of slots < R
+    __shared__ unsigned counts[4];                   // of this block: > T, = T, the same below R
+    __shared__ int sh_latest;
     constexpr int TURN = SEL_T * E;
-    const int unit = blockIdx.x, b = unit / a.H;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int units = a.B * a.H;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if ((int)blockIdx.x >= units * cluster) {
+        // what the slots below R have; moved rows replace theirs in the kernel after this one
+        const int copies = gridDim.x - units * cluster, at = blockIdx.x - units * cluster;
+        for (int unit = at; unit < units; unit += copies) {
+            const int b = unit / a.H;
+            const int n = min(max(a.lens ? a.lens[b] : a.rows, 0), a.rows), R = min(n, a.budget);
+            const long long base = (long long)unit * a.rows;
+            for (int i0 = 0; i0 < R; i0 += 8 * SEL_T) {
+                float m[8];
+                int p[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const int i = i0 + x * SEL_T + tid;
+                    m[x] = i < R ? a.mass[base + i] : 0.f;
+                    p[x] = i < R ? a.pos[base + i] : 0;
+                }
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const int i = i0 + x * SEL_T + tid;
+                    if (i < R) {
+                        a.mass_out[base + i] = m[x];
+                        a.pos_out[base + i] = p[x];
+                    }
+                }
+            }
+        }
+        return;
+    }
+    const int rank = cluster > 1 ? (int)(blockIdx.x & (unsigned)(cluster - 1)) : 0;
+    const int unit = blockIdx.x / cluster, b = unit / a.H;
     const int n = min(max(a.lens ? a.lens[b] : a.rows, 0), a.rows);
     const float *mass = a.mass + (long long)unit * a.rows;
     const int *pos = a.pos + (long long)unit * a.rows;
-    float *mass_out = a.mass_out + (long long)unit * a.rows;
-    int *pos_out = a.pos_out + (long long)unit * a.rows;
     int *src = a.moves + (long long)unit * 2 * a.max_moves, *dst = src + a.max_moves;
     const int R = min(n, a.budget);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // what the slots below R have; moved rows replace theirs in the kernel after this one
-    if (mass_out != mass) {
-#pragma unroll 8
-        for (int i = tid; i < R; i += SEL_T) mass_out[i] = mass[i];
-    }
-    if (pos_out != pos) {
-#pragma unroll 8
-        for (int i = tid; i < R; i += SEL_T) pos_out[i] = pos[i];
-    }
-    if (tid == 0) {
+    if (tid == 0 && rank == 0) {
         a.keep[unit] = R;
         if (n <= a.budget) a.n_moves[unit] = 0;
     }
-    if (n <= a.budget) return;
+    if (n <= a.budget) return;                       // all blocks of the cluster
+    // the block's slots: [lo, hi)
+    const int span = ((n + cluster - 1) / cluster + 31) & ~31;
+    const int lo = min(n, rank * span), hi = min(n, lo + span);
+    const bool one = hi - lo <= TURN;
 
-    int latest = -0x7fffffff - 1;
+    // the latest position, and with one turn the weights
+    float wt[E];
+    int ps[E], latest = -0x7fffffff - 1;
+    if (one) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int j = lo + (warp * E + e) * 32 + lane;
+            ps[e] = j < hi ? pos[j] : -0x7fffffff - 1;
+            wt[e] = j < hi ? mass[j] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) latest = max(latest, ps[e]);
+    } else {
 #pragma unroll 8
-    for (int i = tid; i < n; i += SEL_T) latest = max(latest, pos[i]);
+        for (int i = lo + tid; i < hi; i += SEL_T) latest = max(latest, pos[i]);
+    }
+    for (int i = tid; i < 2 * BINS; i += SEL_T) (&hist[0][0])[i] = 0;
     latest = __reduce_max_sync(0xffffffffu, latest);
-    if (lane == 0) sh[warp] = latest;
+    if (lane == 0) sh[warp] = (unsigned)latest;
     __syncthreads();
-    latest = __reduce_max_sync(0xffffffffu, sh[lane]);
+    latest = __reduce_max_sync(0xffffffffu, (int)sh[lane]);
+    if (cluster > 1) {
+        if (tid == 0) sh_latest = latest;
+        __syncthreads();
+        cluster_sync();
+        for (int x = 0; x < cluster; ++x) latest = max(latest, (int)of_rank(&sh_latest, x));
+    }
     latest = latest < a.recent - 0x7fffffff ? -0x7fffffff - 1 : latest - a.recent;
 
     uint32_t key[E];
-    auto fetch = [&](int turn) {                     // slots past n: key 0, and j < n is asked
+    auto fetch = [&](int turn) {                     // slots past hi: key 0, and j < hi is asked
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const int j = turn + (warp * E + e) * 32 + lane;
-            key[e] = j < n ? evict_key(mass[j], pos[j], a.sinks, latest) : 0u;
+            key[e] = j < hi ? evict_key(mass[j], pos[j], a.sinks, latest) : 0u;
         }
     };
-    const bool one = n <= TURN;
-    if (one) fetch(0);
+    if (one) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int j = lo + (warp * E + e) * 32 + lane;
+            key[e] = j < hi ? evict_key(wt[e], ps[e], a.sinks, latest) : 0u;
+        }
+    }
 
     // T by digits; `above` keys exceed the digits found so far
     uint32_t T = 0, mask = 0;
-    int above = 0;
+    unsigned above = 0;
 #pragma unroll 1
     for (int digit = 0; digit < 3; ++digit) {
         const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bits = digit == 2 ? 10 : 11;
-        for (int i = tid; i < BINS; i += SEL_T) hist[i] = 0;
-        __syncthreads();
-        for (int turn = 0; turn < n; turn += TURN) {
+        unsigned *h = hist[digit & 1];
+        for (int turn = lo; turn < hi; turn += TURN) {
             if (!one) fetch(turn);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const int j = turn + (warp * E + e) * 32 + lane;
-                if (turn + (warp * E + e) * 32 >= n) break;
-                const bool in = j < n && (key[e] & mask) == T;
+                const int j0 = turn + (warp * E + e) * 32;
+                if (j0 >= hi) break;
+                const bool in = j0 + lane < hi && (key[e] & mask) == T;
                 const unsigned d = (key[e] >> shift) & ((1u << bits) - 1u);
-                // equal digits in a whole warp (many equal weights): one atomic
-                int same;
-                __match_all_sync(0xffffffffu, in ? d : 0xffffffffu, &same);
-                if (same) {
-                    if (in && lane == 0) atomicAdd(&hist[d], 32u);
+                // one digit in the whole warp (many equal weights): one atomic
+                const unsigned d0 = __shfl_sync(0xffffffffu, d, 0);
+                if (__all_sync(0xffffffffu, in && d == d0)) {
+                    if (lane == 0) atomicAdd(&h[d], 32u);
                 } else if (in) {
-                    atomicAdd(&hist[d], 1u);
+                    atomicAdd(&h[d], 1u);
                 }
             }
         }
         __syncthreads();
+        if (cluster > 1) cluster_sync();
         // bins from the top: thread i has bins 2047 - 2 i and 2046 - 2 i
         const int b0 = BINS - 1 - 2 * tid;
-        const unsigned h0 = hist[b0], h1 = hist[b0 - 1];
+        unsigned h0 = 0, h1 = 0;
+        if (cluster > 1) {
+            for (int x = 0; x < cluster; ++x) {
+                h0 += of_rank(&h[b0], x);
+                h1 += of_rank(&h[b0 - 1], x);
+            }
+        } else {
+            h0 = h[b0];
+            h1 = h[b0 - 1];
+        }
         unsigned sum = h0 + h1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const unsigned x = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += x;
         }
-        if (lane == 31) sh[warp] = (int)sum;
+        if (lane == 31) sh[warp] = sum;
         __syncthreads();
-        unsigned before = lane < warp ? (unsigned)sh[lane] : 0u;
-        before = __reduce_add_sync(0xffffffffu, before);
+        const unsigned before = __reduce_add_sync(0xffffffffu, lane < warp ? sh[lane] : 0u);
         const unsigned upto = above + before + sum, from = upto - h0 - h1;
         if (from < (unsigned)R && upto >= (unsigned)R) {
             const bool first = from + h0 >= (unsigned)R;
             found[0] = (unsigned)(first ? b0 : b0 - 1);
             found[1] = first ? from : from + h0;
         }
+        // this buffer is used again by the third digit, which all blocks begin after the second's
+        // cluster barrier: no block then reads the first's counts
         __syncthreads();
+        if (digit == 1)
+            for (int i = tid; i < BINS; i += SEL_T) hist[0][i] = 0;
         T |= found[0] << shift;
-        above = (int)found[1];
+        above = found[1];
         mask |= ((1u << bits) - 1u) << shift;
+        __syncthreads();
     }
-    const int ties = R - above;                      // keys equal to T that stay: the lowest slots
+    const int ties = R - (int)above;                 // keys equal to T that stay: the lowest slots
 
-    // kept rows before each warp's runs, turn by turn
+    // counts of this block, then of the blocks before it and of all
+    if (tid < 4) counts[tid] = 0;
+    __syncthreads();
+    for (int turn = lo; turn < hi; turn += TURN) {
+        if (!one) fetch(turn);
+        int c[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int j = turn + (warp * E + e) * 32 + lane;
+            const bool gt = j < hi && key[e] > T, eq = j < hi && key[e] == T;
+            c[0] += gt;
+            c[1] += eq;
+            c[2] += gt && j < R;
+            c[3] += eq && j < R;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            c[x] = __reduce_add_sync(0xffffffffu, c[x]);
+            if (lane == 0 && c[x]) atomicAdd(&counts[x], (unsigned)c[x]);
+        }
+    }
+    __syncthreads();
+    int gt_before = 0, eq_before = 0, low_gt = (int)counts[2], low_eq = (int)counts[3];
+    if (cluster > 1) {
+        cluster_sync();
+        low_gt = low_eq = 0;
+        for (int x = 0; x < cluster; ++x) {
+            if (x < rank) {
+                gt_before += (int)of_rank(&counts[0], x);
+                eq_before += (int)of_rank(&counts[1], x);
+            }
+            low_gt += (int)of_rank(&counts[2], x);
+            low_eq += (int)of_rank(&counts[3], x);
+        }
+        cluster_sync();                              // no block ends while others read its counts
+    }
+    const int low = low_gt + min(low_eq, ties);      // kept rows of slots < R
     const unsigned below = (1u << lane) - 1u;
-    int gt_before = 0, eq_before = 0;                // of the turns before
-    if (tid == 0) kept_low = 0;
-    for (int pass = 0; pass < 2; ++pass) {           // 0: kept_low; 1: the lists
-        gt_before = eq_before = 0;
-        for (int turn = 0; turn < n; turn += TURN) {
-            if (!one) fetch(turn);
-            int gt = 0, eq = 0;
+    for (int turn = lo; turn < hi; turn += TURN) {
+        if (!one) fetch(turn);
+        int gt = 0, eq = 0;
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int j = turn + (warp * E + e) * 32 + lane;
-                gt += j < n && key[e] > T;
-                eq += j < n && key[e] == T;
-            }
-            gt = __reduce_add_sync(0xffffffffu, gt);
-            eq = __reduce_add_sync(0xffffffffu, eq);
-            __syncthreads();
-            if (lane == 0) {
-                sh[warp] = gt;
-                sh2[warp] = eq;
-            }
-            __syncthreads();
-            int g0 = gt_before + __reduce_add_sync(0xffffffffu, lane < warp ? sh[lane] : 0);
-            int e0 = eq_before + __reduce_add_sync(0xffffffffu, lane < warp ? sh2[lane] : 0);
-            gt_before += __reduce_add_sync(0xffffffffu, sh[lane]);
-            eq_before += __reduce_add_sync(0xffffffffu, sh2[lane]);
-            const int run = turn + warp * E * 32;    // the warp's first slot
-            if (pass == 0) {
-                // the warp with slot R counts the kept rows before it
-                if (run <= R && R < run + E * 32) {
-                    int low_gt = 0, low_eq = 0;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const int j = run + e * 32 + lane;
-                        low_gt += j < R && key[e] > T;
-                        low_eq += j < R && key[e] == T;
-                    }
-                    low_gt = g0 + __reduce_add_sync(0xffffffffu, low_gt);
-                    low_eq = e0 + __reduce_add_sync(0xffffffffu, low_eq);
-                    if (lane == 0) kept_low = low_gt + min(low_eq, ties);
-                }
-                continue;
-            }
-            const int low = kept_low;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int j = run + e * 32 + lane;
-                if (run + e * 32 >= n) break;
-                const bool is_gt = j < n && key[e] > T, is_eq = j < n && key[e] == T;
-                const unsigned mg = __ballot_sync(0xffffffffu, is_gt);
-                const unsigned me = __ballot_sync(0xffffffffu, is_eq);
-                const int eq_at = e0 + __popc(me & below);
-                const int kept_at = g0 + __popc(mg & below) + min(eq_at, ties);   // before slot j
-                const bool kept = is_gt || (is_eq && eq_at < ties);
-                if (j < R && !kept) dst[j - kept_at] = j;
-                if (j >= R && kept) src[kept_at - low] = j;
-                g0 += __popc(mg);
-                e0 += __popc(me);
-            }
+        for (int e = 0; e < E; ++e) {
+            const int j = turn + (warp * E + e) * 32 + lane;
+            gt += j < hi && key[e] > T;
+            eq += j < hi && key[e] == T;
+        }
+        gt = __reduce_add_sync(0xffffffffu, gt);
+        eq = __reduce_add_sync(0xffffffffu, eq);
+        __syncthreads();
+        if (lane == 0) {
+            sh[warp] = (unsigned)gt;
+            sh2[warp] = (unsigned)eq;
         }
         __syncthreads();
+        int g0 = gt_before + (int)__reduce_add_sync(0xffffffffu, lane < warp ? sh[lane] : 0u);
+        int e0 = eq_before + (int)__reduce_add_sync(0xffffffffu, lane < warp ? sh2[lane] : 0u);
+        gt_before += (int)__reduce_add_sync(0xffffffffu, sh[lane]);
+        eq_before += (int)__reduce_add_sync(0xffffffffu, sh2[lane]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int j0 = turn + (warp * E + e) * 32, j = j0 + lane;
+            if (j0 >= hi) break;
+            const bool is_gt = j < hi && key[e] > T, is_eq = j < hi && key[e] == T;
+            const unsigned mg = __ballot_sync(0xffffffffu, is_gt);
+            const unsigned me = __ballot_sync(0xffffffffu, is_eq);
+            const int eq_at = e0 + __popc(me & below);
+            const int kept_at = g0 + __popc(mg & below) + min(eq_at, ties);   // before slot j
+            const bool kept = is_gt || (is_eq && eq_at < ties);
+            if (j < min(R, hi) && !kept) dst[j - kept_at] = j;
+            if (j >= R && kept) src[kept_at - low] = j;
+            g0 += __popc(mg);
+            e0 += __popc(me);
+        }
     }
-    if (tid == 0) a.n_moves[unit] = R - kept_low;
+    if (tid == 0 && rank == 0) a.n_moves[unit] = R - low;
 }
 
 // Block (x, unit): the unit's moves, 16 bytes of a key or value row per thread, MOVE_ROWS in flight.
@@ -216,7 +303,6 @@ __global__ void __launch_bounds__(MOVE_T) evict_move_kernel(EvictArgs a, int vec
     if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) a.lens_out[b] = a.keep[unit];
     const int n = a.n_moves[unit];
     const int *src = a.moves + (long long)unit * 2 * a.max_moves, *dst = src + a.max_moves;
-    const long long at = (long long)unit * a.rows;
     // a row has `vecs` 16-byte pieces (16 or 32); keys and values are its two halves
     const int per_row = 2 * vecs, total = n * per_row;
     char *kb = a.k + b * a.seq_st + h * a.head_st, *vb = a.v + b * a.seq_st + h * a.head_st;
@@ -232,16 +318,21 @@ __global__ void __launch_bounds__(MOVE_T) evict_move_kernel(EvictArgs a, int vec
                 const int r = e / per_row, w = e - r * per_row;
                 char *rows = w < vecs ? kb : vb;
                 const int off = (w < vecs ? w : w - vecs) * 16;
-                const int s = src[r], d = dst[r];
-                x[i] = *reinterpret_cast<const uint4 *>(rows + s * a.row_st + off);
-                to[i] = rows + d * a.row_st + off;
-                if (w == 0) a.mass_out[at + d] = a.mass[at + s];
-                if (w == vecs) a.pos_out[at + d] = a.pos[at + s];
+                x[i] = *reinterpret_cast<const uint4 *>(rows + src[r] * a.row_st + off);
+                to[i] = rows + dst[r] * a.row_st + off;
             }
         }
 #pragma unroll
         for (int i = 0; i < MOVE_ROWS; ++i)
             if (to[i]) *reinterpret_cast<uint4 *>(to[i]) = x[i];
+    }
+    const long long at = (long long)unit * a.rows;
+    for (int i = blockIdx.x * MOVE_T + threadIdx.x; i < n; i += stride) {
+        const int s = src[i], d = dst[i];
+        const float m = a.mass[at + s];
+        const int p = a.pos[at + s];
+        a.mass_out[at + d] = m;
+        a.pos_out[at + d] = p;
     }
 }
 
@@ -249,9 +340,30 @@ __global__ void __launch_bounds__(MOVE_T) evict_move_kernel(EvictArgs a, int vec
 
 cudaError_t launch_evict(const EvictArgs &a, int sms, cudaStream_t s) {
     const int units = a.B * a.H;
-    if (a.rows <= 8 * SEL_T) evict_select_kernel<8><<<units, SEL_T, 0, s>>>(a);
-    else evict_select_kernel<32><<<units, SEL_T, 0, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    // long rows and few units: up to four blocks share a unit. Clusters fill a whole number of
+    // blocks, so the copying blocks come in clusters as well.
+    int cluster = 1;
+    while (cluster < 4 && a.rows > 8 * SEL_T * cluster && units * 2 * cluster <= sms) cluster *= 2;
+    int copies = 0;
+    if (a.mass_out != a.mass || a.pos_out != a.pos) {
+        copies = sms - units * cluster;
+        if (copies < 16) copies = 16;
+        if (copies > units) copies = units;
+        copies = (copies + cluster - 1) / cluster * cluster;
+    }
+    cudaLaunchConfig_t sel = {};
+    sel.gridDim = dim3(units * cluster + copies);
+    sel.blockDim = dim3(SEL_T);
+    sel.stream = s;
+    cudaLaunchAttribute cl;
+    cl.id = cudaLaunchAttributeClusterDimension;
+    cl.val.clusterDim.x = cluster;
+    cl.val.clusterDim.y = cl.val.clusterDim.z = 1;
+    sel.attrs = &cl;
+    sel.numAttrs = cluster > 1 ? 1 : 0;
+    const cudaError_t e = a.rows <= 8 * SEL_T * cluster
+                              ? cudaLaunchKernelEx(&sel, evict_select_kernel<8>, a, cluster)
+                              : cudaLaunchKernelEx(&sel, evict_select_kernel<16>, a, cluster);
     if (e != cudaSuccess) return e;
     const int vecs = a.esz == 2 ? 16 : 32;
     const long long want = ((long long)a.max_moves * 2 * vecs + MOVE_T * MOVE_ROWS - 1) /

@@ -213,6 +213,8 @@ EVICT_CASES = [
     (3, 2, 1000, 500, 1, 0, "f32", [1000, 500, 501]), (2, 1, 257, 256, 256, 0, "bf16", None),
     (2, 2, 64, 64, 8, 8, "bf16", [64, 0]), (1, 2, 5000, 100, 64, 36, "bf16", None),
     (2, 2, 4099, 4000, 100, 4, "f32", [4099, 4050]), (1, 1, 60000, 59000, 64, 4, "bf16", None),
+    (2, 2, 33000, 16001, 64, 4, "bf16", [33000, 20000]), (40, 2, 17000, 16500, 1, 0, "bf16", None),
+    (1, 2, 140000, 70000, 64, 4, "bf16", None),
 ]
 
 
