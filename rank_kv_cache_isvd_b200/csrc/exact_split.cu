@@ -9,15 +9,7 @@
 // flight. (Loads by cp.async, one per 16 bytes, cost 750 instructions per warp and step, two thirds
 // of them for addresses: 220 us at 8 x 32768 rows of 8 kv-heads.)
 //
-// Products run on mma.sync m16n8k16 (bf16): a tile of 8 query rows fills half of its 16 rows, and
-// tcgen05 would want 64 or 128. Float32 operands are split in three bf16 terms (24 bits), x = hi +
-// mid + lo: hi sits in rows 0-7 of the A operand and mid in rows 8-15, so one instruction does both
-// terms and both sums land in one thread; lo takes a second one. The same for the weights p, so
-// that float32 outputs keep float32 accuracy (a weight rounded to bf16 would cost 2^-9).
-//
-// Tensor cores truncate where they add, always toward zero: over the hundred steps of a long cache
-// the outputs lost 4e-6. So each step's products start from zero and are added to the outputs in
-// float32 arithmetic (round to nearest), smallest terms first: 8e-7 at 8 x 32768 rows.
+// The products of a warp's 8 query rows are in exact_warp.cuh.
 //
 // By items: a team of warps takes whole items. Short ones go to teams of 1, 2 or 4 warps (a block
 // then works on several, and few warps wait for one another), long ones to a block or a cluster of
@@ -30,107 +22,19 @@
 #include <string.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "exact.cuh"
-#include "tc_util.cuh"
+#include "exact_warp.cuh"
 
 namespace iskv {
 namespace {
 
 constexpr int UNITS = 3;               // of a warp's ring: keys, values, keys, ... of its steps
-constexpr int UNIT = 8192;             // bytes: 32 bf16 rows or 16 float32 rows
 constexpr int RED = EX_D + 8;          // stride of joined rows: the warps' stores meet no conflicts
-constexpr uint32_t POLLS = 1u << 18, SUSPEND_NS = 20000;
 
 __device__ int g_split_status;
 
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ float2 lds2(uint32_t addr) {
-    float2 f;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f.x), "=f"(f.y) : "r"(addr) : "memory");
-    return f;
-}
-__device__ __forceinline__ float lds1(uint32_t addr) {
-    float f;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(addr) : "memory");
-    return f;
-}
-// c += A B with A = 16 x 16, B = 16 x 8, bf16. This thread's A registers: row lane/4 (a0, a2) and
-// row lane/4 + 8 (a1, a3), columns 2 (lane%4) + {0, 1} (a0, a1) and + 8 (a2, a3).
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                    uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// c = A B
-__device__ __forceinline__ void mma0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                     uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ uint32_t pack(float x, float y) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ float lo_of(uint32_t p) { return __uint_as_float(p << 16); }
-__device__ __forceinline__ float hi_of(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
-// (x, y) = sum of three pairs of bf16, each the rounding of what the ones before leave.
-__device__ __forceinline__ void split3(float x, float y, uint32_t &h, uint32_t &m, uint32_t &l) {
-    h = pack(x, y);
-    const float rx = x - lo_of(h), ry = y - hi_of(h);
-    m = pack(rx, ry);
-    l = pack(rx - lo_of(m), ry - hi_of(m));
-}
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, int row, int head,
-                                            int seq, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(0), "r"(head), "r"(seq), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
-    for (uint32_t i = 0; i < POLLS; ++i) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(bar), "r"(parity), "r"(SUSPEND_NS)
-            : "memory");
-        if (done) return true;
-    }
-    return false;
-}
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
@@ -154,7 +58,6 @@ __device__ __forceinline__ float4 ldc4(uint32_t a) {
                  : "memory");
     return f;
 }
-__device__ __forceinline__ float inverse(float l) { return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l); }
 
 // Where an item's rows and queries are. Its visible rows in an order without the gap between sinks
 // and window: c < skp (sk of them, filled up to a multiple of 32) are the sinks, then the rows from
@@ -332,10 +235,8 @@ struct Walk {
 template <bool F32ROWS, bool F32IO, bool MASS>
 __global__ void __launch_bounds__(32 * EX_WARPS, 1)
 exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ ExactMaps maps) {
-    constexpr int WR = ex_warp_rows(F32ROWS);
-    constexpr int NT = WR / 8;                       // groups of 8 rows: columns of a product S
-    constexpr int PARTS = F32ROWS ? 4 : 2;           // 128-byte parts of a row
-    constexpr int PART = UNIT / PARTS;
+    using Rows = WarpRows<F32ROWS, F32IO>;
+    constexpr int WR = Rows::WR, NT = Rows::NT;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -433,10 +334,8 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) load();
 
-        // fragment addresses: 128-byte rows of a part, whose 16-byte chunks are permuted by row
-        const int kr = (lane & 7) + ((lane >> 4) << 3), vr = lane & 15;
-        const uint32_t k_at = kr * 128 + ((((lane >> 3) & 1) ^ (kr & 7)) << 4);
-        const uint32_t v_at = vr * 128 + (((lane >> 4) ^ (vr & 7)) << 4);
+        Rows x8;
+        x8.init();
         uint32_t unit = 0, parity = 0;
         auto taken = [&]() {                         // the unit in use is free: refill it
             __syncwarp();
@@ -450,9 +349,6 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
 
         while (have) {
             const Item it = w.it;
-            uint32_t qh[8][2], qm[F32IO ? 8 : 1][2], ql[F32IO ? 8 : 1][2];
-            float2 o[16];
-            float m = -CUDART_INF_F, l = 0.f;
             const int ti = it.i0 + tok;
             const bool live = ti < it.i1;
             const int pos = it.n - it.ql + ti;       // position of this lane's query row
@@ -460,21 +356,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
             if (live)
                 qp += (it.b < 0 ? ti : it.b) * a.q_seq + (it.h * a.G + head) * a.q_head +
                       (it.b < 0 ? 0 : ti) * a.q_tok;
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int d = ks * 16 + x * 8 + 2 * t;
-                    if constexpr (F32IO) {
-                        float2 f = make_float2(0.f, 0.f);
-                        if (live) f = *reinterpret_cast<const float2 *>(qp + d * 4);
-                        split3(f.x, f.y, qh[ks][x], qm[ks][x], ql[ks][x]);
-                    } else {
-                        qh[ks][x] = live ? *reinterpret_cast<const uint32_t *>(qp + d * 2) : 0u;
-                    }
-                }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = make_float2(0.f, 0.f);
+            x8.begin(qp, live);
             // one token: every row of the order is visible to it, up to C and outside the filling
             const bool plain = it.b < 0 || it.i1 - it.i0 == 1;
 
@@ -484,79 +366,8 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                 const bool sinks = c0 < it.skp;
                 const int seen = min(WR, (sinks ? it.sk : it.C) - c0);   // rows with a row behind
                 late |= !wait_for(bar + unit * 8, parity);
-                const uint32_t kb_ = ring + unit * UNIT;
-                float s[NT][2];                      // scores of row g at columns 8 nt + 2 t + x
-                if constexpr (!F32ROWS) {
-                    // two chains of products per 8 rows, so that few wait on one another
-                    float c[NT][4], e[F32IO ? NT : 1][4];
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-#pragma unroll
-                        for (int np = 0; np < NT / 2; ++np) {
-                            uint32_t kb[4];
-                            ldsm4(kb_ + (ks >> 2) * PART + np * 2048 + (k_at ^ ((ks & 3) << 5)), kb);
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const int nt = 2 * np + y;
-                                const uint32_t b0 = kb[2 * y], b1 = kb[2 * y + 1];
-                                if constexpr (F32IO) {
-                                    if (ks == 0) {
-                                        mma0(e[nt], ql[ks][0], 0u, ql[ks][1], 0u, b0, b1);
-                                        mma0(c[nt], qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], b0, b1);
-                                    } else {
-                                        mma(e[nt], ql[ks][0], 0u, ql[ks][1], 0u, b0, b1);
-                                        mma(c[nt], qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], b0, b1);
-                                    }
-                                } else {
-                                    if (ks == 0) mma0(c[nt], qh[ks][0], 0u, qh[ks][1], 0u, b0, b1);
-                                    else mma(c[nt], qh[ks][0], 0u, qh[ks][1], 0u, b0, b1);
-                                }
-                            }
-                        }
-                    // rows 8-15 hold the mid terms' sums
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            s[nt][x] = F32IO ? (e[nt][x] + c[nt][2 + x]) + c[nt][x] : c[nt][x];
-                } else {
-                    // the large products restart every 32 channels and are summed in float32
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float e[4];                  // the small ones
-                        s[nt][0] = s[nt][1] = 0.f;
-#pragma unroll
-                        for (int kp = 0; kp < 4; ++kp) {
-                            float c[4];
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const int ks = 2 * kp + y, r = nt * 8 + g;
-                                uint32_t kh[2], km[2], kl[2];
-#pragma unroll
-                                for (int x = 0; x < 2; ++x) {
-                                    const int ch = (y * 4 + 2 * x + (t >> 1)) ^ (r & 7);
-                                    const float2 f =
-                                        lds2(kb_ + kp * PART + r * 128 + ch * 16 + (t & 1) * 8);
-                                    split3(f.x, f.y, kh[x], km[x], kl[x]);
-                                }
-                                if (ks == 0)
-                                    mma0(e, qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], kl[0], kl[1]);
-                                else
-                                    mma(e, qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], kl[0], kl[1]);
-                                mma(e, ql[ks][0], 0u, ql[ks][1], 0u, kh[0], kh[1]);
-                                mma(e, qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], km[0], km[1]);
-                                if (y == 0)
-                                    mma0(c, qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], kh[0], kh[1]);
-                                else
-                                    mma(c, qh[ks][0], qm[ks][0], qh[ks][1], qm[ks][1], kh[0], kh[1]);
-                            }
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) s[nt][x] += c[x] + c[2 + x];
-                        }
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) s[nt][x] += e[x] + e[2 + x];
-                    }
-                }
+                float s[NT][2];                      // scores of row g at 8 nt + 2 t + x
+                x8.scores(ring + unit * UNIT, s);
                 taken();
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -574,9 +385,6 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                             if (!see) s[nt][x] = -CUDART_INF_F;
                         }
                 }
-                float top = -CUDART_INF_F;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) top = fmaxf(top, fmaxf(s[nt][0], s[nt][1]));
                 if constexpr (MASS) {
                     if (g < a.G) {
                         float *sc = a.scores +
@@ -586,108 +394,20 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                             *reinterpret_cast<float2 *>(sc + 8 * nt) = make_float2(s[nt][0], s[nt][1]);
                     }
                 }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // The reference m moves only when a score passes it by 2^8: p stays below 256, and
-                // the sums keep their float32 accuracy.
-                const bool raise = top > m + 8.f || (m == -CUDART_INF_F && top > m);
-                if (__any_sync(0xffffffffu, raise)) {
-                    const float nm = raise ? top : m;
-                    const float f = m == -CUDART_INF_F ? 0.f : ex2(m - nm);
-                    m = nm;
-                    l *= f;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        o[i].x *= f;
-                        o[i].y *= f;
-                    }
-                }
-                const float ref = m == -CUDART_INF_F ? 0.f : m;
-                uint32_t ph[NT], pm[NT], pl[NT];
-                float add = 0.f;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float x = ex2(s[nt][0] - ref), y = ex2(s[nt][1] - ref);
-                    add += x + y;
-                    split3(x, y, ph[nt], pm[nt], pl[nt]);
-                }
-                l += add;
-
+                x8.weights(s);
                 late |= !wait_for(bar + unit * 8, parity);
-                const uint32_t vb_ = ring + unit * UNIT;
-                if (seen < WR) {
-                    // values of rows that nobody sees may be anything: 0 x NaN would reach o
-                    for (int r = seen; r < WR; ++r)
-                        if (lane < 8 * PARTS)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                             vb_ + (lane >> 3) * PART + r * 128 + (lane & 7) * 16),
-                                         "r"(0)
-                                         : "memory");
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                if constexpr (!F32ROWS) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        uint32_t vb[NT / 2][4];
-#pragma unroll
-                        for (int kp = 0; kp < NT / 2; ++kp)
-                            ldsm4t(vb_ + (i >> 2) * PART + kp * 2048 + (v_at ^ ((i & 3) << 5)), vb[kp]);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            float c[4];
-                            if constexpr (F32IO) {
-#pragma unroll
-                                for (int kp = 0; kp < NT / 2; ++kp) {
-                                    const uint32_t b0 = vb[kp][2 * x], b1 = vb[kp][2 * x + 1];
-                                    if (kp == 0) mma0(c, pl[0], 0u, pl[1], 0u, b0, b1);
-                                    else mma(c, pl[2 * kp], 0u, pl[2 * kp + 1], 0u, b0, b1);
-                                }
-                            }
-#pragma unroll
-                            for (int kp = 0; kp < NT / 2; ++kp) {
-                                const uint32_t b0 = vb[kp][2 * x], b1 = vb[kp][2 * x + 1];
-                                if (kp == 0 && !F32IO) mma0(c, ph[0], pm[0], ph[1], pm[1], b0, b1);
-                                else mma(c, ph[2 * kp], pm[2 * kp], ph[2 * kp + 1], pm[2 * kp + 1], b0, b1);
-                            }
-                            o[2 * i + x] = add2(o[2 * i + x],
-                                                add2(make_float2(c[0], c[1]), make_float2(c[2], c[3])));
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        uint32_t vh[2], vm[2], vl[2];
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            float f[2];
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const int r = 8 * x + 2 * t + y;
-                                const int ch = ((i & 3) * 2 + (g >> 2)) ^ (r & 7);
-                                f[y] = lds1(vb_ + (i >> 2) * PART + r * 128 + ch * 16 + (g & 3) * 4);
-                            }
-                            split3(f[0], f[1], vh[x], vm[x], vl[x]);
-                        }
-                        float c[4];
-                        mma0(c, ph[0], pm[0], ph[1], pm[1], vl[0], vl[1]);
-                        mma(c, pl[0], 0u, pl[1], 0u, vh[0], vh[1]);
-                        mma(c, ph[0], pm[0], ph[1], pm[1], vm[0], vm[1]);
-                        mma(c, ph[0], pm[0], ph[1], pm[1], vh[0], vh[1]);
-                        o[i] = add2(o[i], add2(make_float2(c[0], c[1]), make_float2(c[2], c[3])));
-                    }
-                }
+                if (seen < WR) Rows::clear(ring + unit * UNIT, seen);
+                x8.values(ring + unit * UNIT);
                 taken();
             }
 
             // ---- the team's part of the item is complete: join its warps ------------------------
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            const float l = x8.sum();
             float *mine = red + (warp * EX_QROWS + g) * RED + 2 * t;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) *reinterpret_cast<float2 *>(mine + 8 * i) = o[i];
+            for (int i = 0; i < 16; ++i) *reinterpret_cast<float2 *>(mine + 8 * i) = x8.o[i];
             if (t == 0) {
-                red_m[warp * EX_QROWS + g] = m;
+                red_m[warp * EX_QROWS + g] = x8.m;
                 red_l[warp * EX_QROWS + g] = l;
             }
             team_sync();
@@ -857,36 +577,54 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
             if (MASS && a.by_items) {
                 // the weights of the rows whose scores this team has
                 team_sync();
-                float ref[EX_QROWS], inv[EX_QROWS];
-                const float *sc[EX_QROWS];
-#pragma unroll
-                for (int r = 0; r < EX_QROWS; ++r) {
-                    if (r >= a.G) break;
-                    ref[r] = red_m[team0 * EX_QROWS + r];
-                    inv[r] = inverse(red_l[team0 * EX_QROWS + r]);
-                    sc[r] = a.scores + (((long long)it.b * a.H + it.h) * a.G + r) * a.score_st;
-                }
-                const long long base = ((long long)it.b * a.H + it.h) * a.rows;
                 const int hi = min(it.C, w.s1 * rs);
-                // four rows per thread and turn; scores are padded to whole groups of rows
-#pragma unroll 2
-                for (int j = w.s0 * rs + 4 * (tw * 32 + lane); j < hi; j += 128 * T) {
-                    float x[4] = {0.f, 0.f, 0.f, 0.f}, old[4];
+                const float *sc = a.scores + ((long long)it.b * a.H + it.h) * a.G * a.score_st;
+                const long long base = ((long long)it.b * a.H + it.h) * a.rows;
+                // U groups of four rows per thread and turn, whose loads are in flight together;
+                // scores are padded to whole groups of rows
+                auto add = [&](auto rows_, auto u_) {
+                    constexpr int RN = decltype(rows_)::value, U = decltype(u_)::value;
+                    float ref[RN], inv[RN];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) old[y] = j + y < hi ? a.mass[base + j + y] : 0.f;
-#pragma unroll
-                    for (int r = 0; r < EX_QROWS; ++r) {
-                        if (r >= a.G) break;
-                        const float4 f = *reinterpret_cast<const float4 *>(sc[r] + j);
-                        x[0] += ex2(f.x - ref[r]) * inv[r];
-                        x[1] += ex2(f.y - ref[r]) * inv[r];
-                        x[2] += ex2(f.z - ref[r]) * inv[r];
-                        x[3] += ex2(f.w - ref[r]) * inv[r];
+                    for (int r = 0; r < RN; ++r) {
+                        ref[r] = r < a.G ? red_m[team0 * EX_QROWS + r] : 0.f;
+                        inv[r] = r < a.G ? inverse(red_l[team0 * EX_QROWS + r]) : 0.f;
                     }
+                    const int j0 = w.s0 * rs + 4 * (tw * 32 + lane), step = 128 * T;
+                    for (int j = j0; j < hi; j += U * step) {
+                        float4 f[U][RN];
+                        float old[U][4];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        if (j + y < hi) a.mass_out[base + j + y] = old[y] + x[y];
-                }
+                        for (int u = 0; u < U; ++u) {
+                            const int at = j + u * step;
+#pragma unroll
+                            for (int r = 0; r < RN; ++r)
+                                f[u][r] = at < hi && r < a.G
+                                              ? *reinterpret_cast<const float4 *>(sc + r * a.score_st + at)
+                                              : make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F,
+                                                            -CUDART_INF_F);
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                old[u][y] = at + y < hi ? a.mass[base + at + y] : 0.f;
+                        }
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const int at = j + u * step;
+#pragma unroll
+                            for (int r = 0; r < RN; ++r) {
+                                old[u][0] += ex2(f[u][r].x - ref[r]) * inv[r];
+                                old[u][1] += ex2(f[u][r].y - ref[r]) * inv[r];
+                                old[u][2] += ex2(f[u][r].z - ref[r]) * inv[r];
+                                old[u][3] += ex2(f[u][r].w - ref[r]) * inv[r];
+                            }
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                if (at + y < hi) a.mass_out[base + at + y] = old[u][y];
+                        }
+                    }
+                };
+                if (a.G <= 4) add(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
+                else add(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
             }
             team_sync();                             // what joined may be overwritten
             if (parts > 1) cluster_sync();
