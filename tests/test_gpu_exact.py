@@ -415,7 +415,7 @@ def test_small_workspaces_and_wrong_tensors_are_refused():
                 torch.zeros((1, 2, 64), dtype=torch.int32, device="cuda"), budget=8, recent=1)
     with pytest.raises(ValueError):
         c.prefix_decode(q[:, :, 0], k[0].float(), v[0].float())
-    form = c._queries[(q.shape, q.stride(), ok.stride(), q.dtype, True)][0]
+    form = iskv.iskv_exact_queries(0, 0, 8 * D, D, D, 8 * D, D, D, 8, 1, iskv.ISKV_F32, None)
     form.q, form.out = q.data_ptr(), ok.data_ptr()
     code, need = iskv.iskv_window_attn_workspace(c._rows, form, 8, 0)
     assert code == 0
