@@ -199,26 +199,28 @@ bool prefix_maps(CUtensorMap *k, CUtensorMap *v, const iskv_exact_rows *r,
 }
 
 struct TilePlan {
-    bool use, alternate;
+    bool use, tile, alternate;         // tile: by the tile kernel, else by the rows kernel
     int tq, pairs, nsp;
 };
 
 // `tokens` query tokens (prefix: sequences) per unit, over at most `seen` rows each.
-TilePlan tile_plan(int units, int tokens, int G, long long seen, int sms) {
+TilePlan tile_plan(int units, int tokens, int G, long long seen, bool tile, int sms) {
     TilePlan p;
     memset(&p, 0, sizeof(p));
     // one tile of 8 query rows reads the rows once in the split kernel as well
     p.use = tokens * (long long)G > EX_QROWS && seen > 0;
     if (!p.use) return p;
-    p.tq = TILE_ROWS / G;
+    p.tile = tile;
+    p.tq = tile ? TILE_ROWS / G : EX_WARPS * ex_tpt(G);
     const long long tiles = (tokens + p.tq - 1) / p.tq;
-    p.alternate = tiles == 1;                 // one tile: the CTA's halves share out its blocks
-    p.pairs = (int)(p.alternate ? 1 : (tiles + 1) / 2);
+    p.alternate = tile && tiles == 1;         // one tile: the CTA's halves share out its blocks
+    p.pairs = (int)(!tile || p.alternate ? tiles : (tiles + 1) / 2);
     const long long ctas = (long long)units * p.pairs;
     const long long blocks = (seen + TILE_ROWS - 1) / TILE_ROWS;
-    // fewer CTAs than SMs: split the rows, in parts of four blocks at least
+    // fewer CTAs than SMs: split the rows, in parts of a few blocks at least (a CTA's beginning and
+    // end take the time of about four blocks of the tile kernel, of one of the rows kernel)
     long long nsp = ctas >= sms ? 1 : sms / ctas;
-    const long long most = blocks / 4 > 1 ? blocks / 4 : 1;
+    const long long most = blocks / (tile ? 4 : 1) > 1 ? blocks / (tile ? 4 : 1) : 1;
     if (nsp > most) nsp = most;
     p.nsp = (int)(nsp < EX_PRE_MAX ? nsp : EX_PRE_MAX);
     return p;
@@ -234,25 +236,19 @@ bool all_bf16(const iskv_exact_rows *r, const iskv_exact_queries *q) {
 }
 
 TilePlan window_plan(const iskv_exact_rows *r, const iskv_exact_queries *q, int window, int sinks,
-                     int sms) {
-    TilePlan none;
-    memset(&none, 0, sizeof(none));
-    if (!all_bf16(r, q)) return none;
+                     bool tile, int sms) {
     const int G = q->n_q_heads / r->n_kv_heads;
     // rows that a pair of tiles sees at most
     const long long near = (long long)window + sinks + 2 * (TILE_ROWS / G);
-    return tile_plan(r->batch * r->n_kv_heads, q->m, G, near < r->rows ? near : r->rows, sms);
+    return tile_plan(r->batch * r->n_kv_heads, q->m, G, near < r->rows ? near : r->rows, tile, sms);
 }
 
 TilePlan prefix_plan(const iskv_exact_rows *r, const iskv_exact_queries *q,
-                     const iskv_exact_prefix *p, int sms) {
-    TilePlan none;
-    memset(&none, 0, sizeof(none));
-    if (!all_bf16(r, q)) return none;
-    return tile_plan(r->n_kv_heads, r->batch, q->n_q_heads / r->n_kv_heads, p->rows, sms);
+                     const iskv_exact_prefix *p, bool tile, int sms) {
+    return tile_plan(r->n_kv_heads, r->batch, q->n_q_heads / r->n_kv_heads, p->rows, tile, sms);
 }
 
-// The tile kernel's arguments.
+// Arguments of the kernels for many rows.
 void tile_args(TileArgs &t, const TilePlan &p, const ExactArgs &a, bool prefix, float *records) {
     memset(&t, 0, sizeof(t));
     t.B = a.B;
@@ -269,6 +265,10 @@ void tile_args(TileArgs &t, const TilePlan &p, const ExactArgs &a, bool prefix, 
     t.tq = p.tq;
     t.pairs = p.pairs;
     t.nsp = p.nsp;
+    t.q = a.q;
+    t.q_seq = a.q_seq;
+    t.q_head = a.q_head;
+    t.q_tok = a.q_tok;
     t.out = a.out;
     t.o_seq = a.o_seq;
     t.o_head = a.o_head;
@@ -282,7 +282,7 @@ void tile_args(TileArgs &t, const TilePlan &p, const ExactArgs &a, bool prefix, 
 }
 // Queries as (64 channels of a half, q-head, token, sequence), boxes of one group's heads and one
 // tile's tokens (prefix: sequences). False where items share a place: the tile kernel cannot take
-// such queries, and the split kernel does.
+// such queries, and the rows kernel does.
 bool query_map(CUtensorMap *map, const ExactArgs &a, bool prefix, int tq) {
     const long long ext[3] = {(long long)a.H * a.G, a.m, a.B}, st[3] = {a.q_head, a.q_tok, a.q_seq};
     cuuint64_t dims[4] = {EX_D, 0, 0, 0}, strides[3];
@@ -358,13 +358,15 @@ extern "C" int iskv_window_attn_workspace(const iskv_exact_rows *r, const iskv_e
     if (rc != ISKV_OK) return rc;
     const int sms = sm_count();
     if (!sms) return ISKV_ERR_CUDA;
-    const TilePlan p = window_plan(r, q, window, sinks, sms);
-    const size_t split = record_bytes(sms, 0);
-    const size_t tile =
-        p.nsp > 1 ? tile_record_bytes(p, (long long)r->batch * r->n_kv_heads, q->m,
-                                          q->n_q_heads / r->n_kv_heads)
-                      : 0;
-    *bytes = split > tile ? split : tile;
+    const long long units = (long long)r->batch * r->n_kv_heads;
+    const int G = q->n_q_heads / r->n_kv_heads;
+    *bytes = record_bytes(sms, 0);
+    // what the call takes: queries that cannot be mapped go to the rows kernel
+    for (int tile = 0; tile <= (all_bf16(r, q) ? 1 : 0); ++tile) {
+        const TilePlan p = window_plan(r, q, window, sinks, tile != 0, sms);
+        const size_t b = p.nsp > 1 ? tile_record_bytes(p, units, q->m, G) : 0;
+        if (b > *bytes) *bytes = b;
+    }
     return ISKV_OK;
 }
 
@@ -380,15 +382,19 @@ extern "C" int iskv_window_attn(const iskv_exact_rows *r, const iskv_exact_queri
     a.window = window < kMaxRows ? window : (int)kMaxRows;
     a.sinks = sinks < r->rows ? sinks : r->rows;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const TilePlan p = window_plan(r, q, window, sinks, a.grid);
+    const bool fr = r->dtype == ISKV_F32, fi = q->dtype == ISKV_F32;
     CUtensorMap qm, km, vm;
-    if (p.use && query_map(&qm, a, false, p.tq)) {
-        if (!own_maps(&km, &vm, r, TILE_ROWS)) return ISKV_ERR_CUDA;
+    TilePlan p = window_plan(r, q, window, sinks, all_bf16(r, q), a.grid);
+    if (p.tile && !query_map(&qm, a, false, p.tq))
+        p = window_plan(r, q, window, sinks, false, a.grid);
+    if (p.use) {
+        if (!own_maps(&km, &vm, r, p.tile ? TILE_ROWS : ex_warp_rows(fr))) return ISKV_ERR_CUDA;
         TileArgs t;
         tile_args(t, p, a, false, p.nsp > 1 ? static_cast<float *>(ws) : nullptr);
-        const int e = launched(launch_exact_tile(t, qm, km, vm, false, p.alternate, s));
+        const int e = launched(p.tile ? launch_exact_tile(t, qm, km, vm, false, p.alternate, s)
+                                      : launch_exact_rows(t, km, vm, fr, fi, false, s));
         if (e != ISKV_OK || p.nsp == 1) return e;
-        return launched(launch_exact_tile_merge(t, s));
+        return launched(launch_exact_tile_merge(t, fi, s));
     }
     a.rec = static_cast<float *>(ws);
     ExactMaps maps;
@@ -446,9 +452,13 @@ extern "C" int iskv_prefix_decode_workspace(const iskv_exact_rows *r, const iskv
     if (!sms) return ISKV_ERR_CUDA;
     const int tpt = ex_tpt(q->n_q_heads / r->n_kv_heads);
     const long long tiles = (r->batch + tpt - 1) / tpt;
-    *bytes = record_bytes(sms, (long long)r->n_kv_heads * (r->batch + tiles)) +
-             tile_record_bytes(prefix_plan(r, q, p, sms), r->n_kv_heads, r->batch,
-                               q->n_q_heads / r->n_kv_heads);
+    size_t records = 0;
+    for (int tile = 0; tile <= (all_bf16(r, q) ? 1 : 0); ++tile) {
+        const size_t b = tile_record_bytes(prefix_plan(r, q, p, tile != 0, sms), r->n_kv_heads,
+                                           r->batch, q->n_q_heads / r->n_kv_heads);
+        if (b > records) records = b;
+    }
+    *bytes = record_bytes(sms, (long long)r->n_kv_heads * (r->batch + tiles)) + records;
     return ISKV_OK;
 }
 
@@ -466,16 +476,20 @@ extern "C" int iskv_prefix_decode(const iskv_exact_rows *r, const iskv_exact_que
     a.p_head_mul = multiplier(p->head_stride, r->n_kv_heads);
     a.rec = static_cast<float *>(ws);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const TilePlan plan = prefix_plan(r, q, p, a.grid);
+    const bool fr = r->dtype == ISKV_F32, fi = q->dtype == ISKV_F32;
     ExactMaps maps;
     CUtensorMap qm, km, vm;
-    if (plan.use && query_map(&qm, a, true, plan.tq)) {
-        if (!prefix_maps(&km, &vm, r, p, TILE_ROWS)) return ISKV_ERR_CUDA;
+    TilePlan plan = prefix_plan(r, q, p, all_bf16(r, q), a.grid);
+    if (plan.tile && !query_map(&qm, a, true, plan.tq)) plan = prefix_plan(r, q, p, false, a.grid);
+    if (plan.use) {
+        if (!prefix_maps(&km, &vm, r, p, plan.tile ? TILE_ROWS : ex_warp_rows(fr)))
+            return ISKV_ERR_CUDA;
         const int tpt = ex_tpt(a.G);
         const size_t at = record_bytes(a.grid, (long long)a.H * (a.B + (a.B + tpt - 1) / tpt));
         TileArgs t;
         tile_args(t, plan, a, true, reinterpret_cast<float *>(static_cast<char *>(ws) + at));
-        const int e = launched(launch_exact_tile(t, qm, km, vm, true, plan.alternate, s));
+        const int e = launched(plan.tile ? launch_exact_tile(t, qm, km, vm, true, plan.alternate, s)
+                                         : launch_exact_rows(t, km, vm, fr, fi, true, s));
         if (e != ISKV_OK) return e;
         a.pre_ml = t.pre_ml;
         a.pre_o = t.pre_o;
@@ -547,8 +561,9 @@ extern "C" int iskv_evict(const iskv_exact_rows *r, const float *mass, float *ma
 
 extern "C" int iskv_exact_status(iskv_stream_t stream) {
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    int tile = 0, split = 0;
+    int tile = 0, rows = 0, split = 0;
     int rc = launched(exact_tile_status(&tile, s));
+    if (rc == ISKV_OK) rc = launched(exact_rows_status(&rows, s));
     if (rc == ISKV_OK) rc = launched(exact_split_status(&split, s));
-    return rc != ISKV_OK ? rc : tile || split ? ISKV_ERR_TIMEOUT : ISKV_OK;
+    return rc != ISKV_OK ? rc : tile || rows || split ? ISKV_ERR_TIMEOUT : ISKV_OK;
 }

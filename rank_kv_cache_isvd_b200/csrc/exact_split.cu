@@ -433,7 +433,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                     *reinterpret_cast<uint2 *>(op + lane * 8) =
                         make_uint2(pack(y.x * inv, y.y * inv), pack(y.z * inv, y.w * inv));
             };
-            const int nsp = finish ? a.nsp : 0;
+            const int nsp = finish && rank == 0 ? a.nsp : 0;   // (one block of a cluster adds them)
             if (nsp) asm volatile("griddepcontrol.wait;" ::: "memory");
             const int used = ex_tpt(a.G) * a.G;
             for (int r = tw; r < (finish ? used : EX_QROWS); r += T) {

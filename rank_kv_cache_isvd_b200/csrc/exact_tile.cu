@@ -653,6 +653,7 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
 }
 
 // Joins the records of split rows: a warp per query row, four channels per lane.
+template <bool F32IO>
 __global__ void __launch_bounds__(256) exact_tile_merge_kernel(const __grid_constant__ TileArgs a) {
     const int lane = threadIdx.x & 31;
     const long long per_unit = (long long)a.m * a.G;
@@ -683,8 +684,12 @@ __global__ void __launch_bounds__(256) exact_tile_merge_kernel(const __grid_cons
     }
     const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
     char *op = a.out + b * a.o_seq + (long long)(h * a.G + g) * a.o_head + tok * a.o_tok;
-    *reinterpret_cast<uint2 *>(op + lane * 8) =
-        make_uint2(pack(o.x * inv, o.y * inv), pack(o.z * inv, o.w * inv));
+    if constexpr (F32IO)
+        *reinterpret_cast<float4 *>(op + lane * 16) =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    else
+        *reinterpret_cast<uint2 *>(op + lane * 8) =
+            make_uint2(pack(o.x * inv, o.y * inv), pack(o.z * inv, o.w * inv));
 }
 
 template <bool PREFIX, bool ALT>
@@ -721,7 +726,7 @@ cudaError_t launch_exact_tile(const TileArgs &a, const CUtensorMap &q, const CUt
     return alternate ? launch<false, true>(a, q, k, v, s) : launch<false, false>(a, q, k, v, s);
 }
 
-cudaError_t launch_exact_tile_merge(const TileArgs &a, cudaStream_t s) {
+cudaError_t launch_exact_tile_merge(const TileArgs &a, bool f32_io, cudaStream_t s) {
     const long long blocks = ((long long)a.B * a.H * a.m * a.G + 7) / 8;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
@@ -733,7 +738,8 @@ cudaError_t launch_exact_tile_merge(const TileArgs &a, cudaStream_t s) {
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, exact_tile_merge_kernel, a);
+    return f32_io ? cudaLaunchKernelEx(&cfg, exact_tile_merge_kernel<true>, a)
+                  : cudaLaunchKernelEx(&cfg, exact_tile_merge_kernel<false>, a);
 }
 
 cudaError_t exact_tile_status(int *timed_out, cudaStream_t s) {

@@ -1,5 +1,5 @@
-// Arguments of the tile kernel (exact_tile.cu): attention of many query rows over exact rows on the
-// tensor cores.
+// Arguments of the kernels for many query rows: the tile kernel (exact_tile.cu: bf16, tcgen05) and
+// the rows kernel (exact_rows.cu: float32 operands).
 #pragma once
 
 #include <cuda.h>
@@ -16,9 +16,11 @@ struct TileArgs {
     int m;                             // tokens per sequence (prefix: sequences)
     int window, sinks;
     int seq_mul, head_mul;             // 0 where all sequences, or kv-heads, share one stream
-    int tq;                            // tokens per tile: 128 / G
-    int pairs;                         // pairs of tiles per (sequence, kv-head)
+    int tq;                            // tokens per tile (rows kernel: per group of 8 tiles)
+    int pairs;                         // pairs of tiles (groups) per (sequence, kv-head)
     int nsp;                           // splits of the rows' blocks
+    const char *q;                     // rows kernel
+    long long q_seq, q_head, q_tok;    // bytes
     char *out;                         // whole results (nsp 1) ...
     long long o_seq, o_head, o_tok;    // bytes
     float *pre_ml, *pre_o;             // ... or records [B H][nsp][m G][2] and [..][128]
@@ -31,10 +33,15 @@ struct TileArgs {
 cudaError_t launch_exact_tile(const TileArgs &a, const CUtensorMap &q, const CUtensorMap &k,
                               const CUtensorMap &v, bool prefix, bool alternate, cudaStream_t s);
 
-// Joins the records of launch_exact_tile (not prefix) with nsp > 1.
-cudaError_t launch_exact_tile_merge(const TileArgs &a, cudaStream_t s);
+// Maps of the rows in boxes of ex_warp_rows() whole rows.
+cudaError_t launch_exact_rows(const TileArgs &a, const CUtensorMap &k, const CUtensorMap &v,
+                              bool f32_rows, bool f32_io, bool prefix, cudaStream_t s);
 
-// Sticky status of the tile kernel's bounded waits on the current device: 0 or 1. Clears it.
+// Joins the records of either (not prefix) with nsp > 1.
+cudaError_t launch_exact_tile_merge(const TileArgs &a, bool f32_io, cudaStream_t s);
+
+// Sticky status of the kernels' bounded waits on the current device: 0 or 1. Clears it.
 cudaError_t exact_tile_status(int *timed_out, cudaStream_t s);
+cudaError_t exact_rows_status(int *timed_out, cudaStream_t s);
 
 }  // namespace iskv

@@ -75,6 +75,10 @@ WINDOW_CASES = [
     (2, 1, 7, 260, 130, 64, 0, "bf16", "bf16", [260, 131], [130, 1], True),
     (1, 1, 1, 900, 300, 128, 128, "bf16", "bf16", None, None, False),
     (1, 3, 6, 150, 40, 150, 200, "bf16", "bf16", None, None, True),
+    (1, 2, 4, 600, 600, 90, 5, "f32", "bf16", None, None, True),
+    (2, 1, 8, 333, 200, 77, 40, "f32", "f32", [333, 150], [200, 150], False),
+    (1, 1, 5, 3000, 30, 1 << 24, 0, "f32", "bf16", None, None, False),
+    (1, 1, 4, 5000, 9, 4000, 100, "bf16", "bf16", None, None, False),
 ]
 
 
@@ -182,6 +186,8 @@ PREFIX_CASES = [
     (70, 2, 1, 333, 9, "bf16", "bf16", None), (65, 1, 7, 640, 3, "bf16", "bf16", None),
     (16, 1, 8, 2100, 5, "bf16", "bf16", None), (300, 1, 2, 128, 1, "bf16", "bf16", None),
     (5, 2, 3, 4000, 33, "bf16", "bf16", [33, 0, 2, 3, 4]),
+    (9, 1, 8, 500, 1500, "bf16", "bf16", None), (40, 1, 4, 1100, 600, "f32", "bf16", None),
+    (150, 1, 2, 257, 40, "f32", "f32", None), (20, 2, 4, 900, 300, "f32", "f32", [300, 1] * 10),
 ]
 
 
