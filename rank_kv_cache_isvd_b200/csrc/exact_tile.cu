@@ -191,6 +191,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
+// The lowest n bits (none below 0, all from 32 on).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
 // What a CTA works on. PREFIX: "tokens" are the batch's sequences, the rows have no sequence, and
 // every row is visible.
 struct Work {
@@ -365,13 +370,14 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
             const bool gap = base <= w.p0 - a.window && base + TILE_ROWS > a.sinks;
             if (!tail && !gap) return;
             uint8_t *v = ring + st * BLOCK_BYTES;
-            for (int r = lane; r < TILE_ROWS; r += 32) {
-                const int j = base + r;
-                if (j <= w.p1 && (j < a.sinks || j > w.p0 - a.window)) continue;
-                for (int x = 0; x < 16; ++x)
-                    *reinterpret_cast<uint4 *>(v + (x >> 3) * HALF_BYTES + r * 128 + (x & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
-            }
+            // rows from r0 to r1 lie together in each half
+            auto zero = [&](int r0, int r1) {
+                for (int x = 0; x < 2; ++x)
+                    for (int e = r0 * 128 + lane * 16; e < r1 * 128; e += 512)
+                        *reinterpret_cast<uint4 *>(v + x * HALF_BYTES + e) = make_uint4(0, 0, 0, 0);
+            };
+            if (tail) zero(max(0, w.p1 + 1 - base), TILE_ROWS);
+            if (gap) zero(max(0, a.sinks - base), min(TILE_ROWS, w.p0 - a.window + 1 - base));
             fence_proxy_async_smem();
             __syncwarp();
         };
@@ -481,12 +487,13 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
                 const int hi = pos - base, lo = PREFIX ? 0 : pos - a.window + 1 - base;
                 const int sk = PREFIX ? 0 : a.sinks - base;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {
+                    // bit e: key 32 c + e is seen
+                    const uint32_t see = bits_below(hi + 1 - 32 * c) &
+                                         (~bits_below(lo - 32 * c) | bits_below(sk - 32 * c));
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int j = c * 32 + e;
-                        if (!(j <= hi && (j >= lo || j < sk))) s[c][e] = -CUDART_INF_F;
-                    }
+                    for (int e = 0; e < 32; ++e) s[c][e] = see & (1u << e) ? s[c][e] : -CUDART_INF_F;
+                }
             }
             float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
