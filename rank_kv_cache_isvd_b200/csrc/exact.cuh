@@ -18,8 +18,7 @@ namespace iskv {
 constexpr int EX_D = 128;
 constexpr int EX_QROWS = 8;            // query rows of a split-kernel tile (tokens x GQA group)
 constexpr int EX_REC = EX_QROWS * (2 + EX_D);   // floats of a record: m[8], l[8], O[8][128]
-constexpr int EX_MAXREC = 1024;        // records that one merge block can combine
-constexpr int EX_PRE_MAX = 32;         // of them at most from the tile kernel
+constexpr int EX_PRE_MAX = 32;         // splits of a shared prefix at most
 
 struct ExactArgs {
     int B, H, rows;
@@ -44,9 +43,9 @@ struct ExactArgs {
     int nsp;                           // their number of splits (0: none)
     float scale_log2;                  // log2(e) / sqrt(128)
     int grid;                          // blocks of the split kernel
-    int by_items;                      // 1: a team of warps takes whole items; 0: a block takes steps
-    int team;                          // by items: warps of a team (1, 2, 4, 8) ...
-    int cluster;                       // ... and (team 8) blocks that share an item's steps
+    int by_items;                      // 1: a team of warps takes whole items; 0: it takes steps
+    int team, teams;                   // warps of a team (1, 2, 4, 8), teams of the grid
+    int cluster;                       // by items, team 8: blocks that share an item's steps
     int rt_max;                        // tiles per (sequence, kv-head) at most
     unsigned items, share, extra;      // by items: their number, and per team; `extra` teams take 1 more
     int after;                         // 1: launched next to the kernel before it, whose end it awaits
@@ -71,8 +70,8 @@ __device__ __forceinline__ int ex_qlen(const ExactArgs &a, int b) {
 
 // Items in order: the shared prefix's (kv-head, tile of 8 (sequence, q-head) rows), then every
 // sequence's (kv-head, tile of 8 (token, q-head) rows). An item takes S steps of `rs` rows.
-// By steps: the flat space of (item, step) is cut into equal ranges, one per block. By items: the
-// list of (sequence, kv-head, tile) is, one range per team of warps or cluster of blocks.
+// By steps: the flat space of (item, step) is cut into equal ranges, one per team of warps. By items:
+// the list of (sequence, kv-head, tile) is, one range per team or cluster of blocks.
 struct ExactSpan {
     int S;            // steps per item (0: there are no items)
     int RT;           // tiles per kv-head
@@ -122,12 +121,9 @@ __device__ __forceinline__ unsigned ex_length(const ExactArgs &a, int seqs, int 
     return t + (unsigned)a.H * p.RT * p.S;
 }
 
-// Warps per block of the split kernel, rows per warp and step, rows per step.
+// Warps per block of the split kernel, rows per warp and step.
 constexpr int EX_WARPS = 8;
 __host__ __device__ constexpr int ex_warp_rows(bool f32_rows) { return f32_rows ? 16 : 32; }
-__host__ __device__ constexpr int ex_step_rows(bool f32_rows) {
-    return EX_WARPS * ex_warp_rows(f32_rows);
-}
 
 cudaError_t launch_exact_split(const ExactArgs &a, const ExactMaps &maps, bool f32_rows, bool f32_io,
                                cudaStream_t s);

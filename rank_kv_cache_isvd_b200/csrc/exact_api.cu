@@ -118,9 +118,9 @@ void fill(ExactArgs &a, const iskv_exact_rows *r, const iskv_exact_queries *q, i
     a.cluster = 1;
 }
 
-// Workspace of the split kernel: its blocks' records, and with `items` one per item as well.
-size_t record_bytes(int grid, long long items) {
-    return align256((size_t)(2LL * grid + items) * EX_REC * sizeof(float));
+// Workspace of the split kernel: its teams' records, and with `items` one per item as well.
+size_t record_bytes(int sms, long long items) {
+    return align256((size_t)(2LL * EX_WARPS * sms + items) * EX_REC * sizeof(float));
 }
 long long score_stride(int rows) { return (rows + 31) / 32 * 32; }
 size_t score_bytes(const iskv_exact_rows *r, int n_q_heads) {
@@ -222,7 +222,8 @@ TilePlan tile_plan(int units, int tokens, int G, long long seen, bool tile, int 
     long long nsp = ctas >= sms ? 1 : sms / ctas;
     const long long most = blocks / (tile ? 4 : 1) > 1 ? blocks / (tile ? 4 : 1) : 1;
     if (nsp > most) nsp = most;
-    p.nsp = (int)(nsp < EX_PRE_MAX ? nsp : EX_PRE_MAX);
+    if (nsp > EX_PRE_MAX) nsp = EX_PRE_MAX;
+    p.nsp = (int)nsp;
     return p;
 }
 size_t tile_record_bytes(const TilePlan &p, long long units, long long tokens, int G) {
@@ -304,12 +305,16 @@ void split_plan(ExactArgs &a, bool f32_rows, int sms) {
     const int tiles = (a.m + tpt - 1) / tpt;
     const long long items = (long long)a.B * a.H * tiles;
     const int most = ex_most_rows(a.window, a.sinks, tpt, a.rows);
-    a.grid = sms;
     a.cluster = 1;
-    a.team = EX_WARPS;
     a.by_items = 0;
     a.rt_max = tiles;
-    if (a.shared_here) return;                       // its tiles and the sequences' join by records
+    auto by_steps = [&](int team) {
+        a.grid = sms;
+        a.team = team;
+        a.teams = sms * (EX_WARPS / team);
+    };
+    // a shared prefix's tiles and the sequences' own rows join by records
+    if (a.shared_here) return by_steps(EX_WARPS);
     // teams as large as there are warps for every item, and no larger than the item has rows for
     int team = EX_WARPS, c = 1;
     while (team > 1 && (items * team > (long long)sms * EX_WARPS || most <= wr * team / 2)) team /= 2;
@@ -325,8 +330,8 @@ void split_plan(ExactArgs &a, bool f32_rows, int sms) {
     const long long rounds = (items + slots - 1) / slots;
     // tiles of one prompt see different numbers of rows; long items in a last, partly filled round
     // leave SMs idle
-    if (tiles > 1 && rounds > 1) return;
-    if (4 * items < 3 * rounds * slots && steps > 8 * c) return;
+    if ((tiles > 1 && rounds > 1) || (4 * items < 3 * rounds * slots && steps > 8 * c))
+        return by_steps(items >= 2 * sms ? 1 : EX_WARPS);
     const long long teams = items < slots ? items : slots;
     a.by_items = 1;
     a.team = team;
@@ -334,17 +339,17 @@ void split_plan(ExactArgs &a, bool f32_rows, int sms) {
     // few items: their teams spread over the SMs
     const int per_block = EX_WARPS / team;
     a.grid = (int)((teams + per_block - 1) / per_block) * c;
-    const long long all = (long long)a.grid / c * per_block;
+    a.teams = a.grid / c * per_block;
     a.items = (unsigned)items;
-    a.share = (unsigned)(items / all);
-    a.extra = (unsigned)(items % all);
+    a.share = (unsigned)(items / a.teams);
+    a.extra = (unsigned)(items % a.teams);
 }
 
 int run_split(ExactArgs &a, ExactMaps &maps, const iskv_exact_rows *r, const iskv_exact_queries *q,
               cudaStream_t s) {
     const bool fr = r->dtype == ISKV_F32, fi = q->dtype == ISKV_F32;
     if (!own_maps(&maps.k, &maps.v, r, ex_warp_rows(fr))) return ISKV_ERR_CUDA;
-    split_plan(a, fr, sm_count());
+    split_plan(a, fr, a.grid);
     const int rc = launched(launch_exact_split(a, maps, fr, fi, s));
     return rc == ISKV_OK ? launched(launch_exact_merge(a, fr, fi, s)) : rc;
 }

@@ -11,13 +11,16 @@
 //
 // The products of a warp's 8 query rows are in exact_warp.cuh.
 //
-// By items: a team of warps takes whole items. Short ones go to teams of 1, 2 or 4 warps (a block
-// then works on several, and few warps wait for one another), long ones to a block or a cluster of
-// up to 8 blocks that share out the item's steps and join their results through distributed shared
-// memory: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i. One launch, no workspace. By steps: the
-// flat space of (item, step) is cut into equal ranges, one per block, so that items of any number
-// and lengths fill the GPU evenly; an item that several blocks share leaves one record per block in
-// global memory, which the merge kernel joins in the same way.
+// Behind a kernel that does a shared prefix (it starts on the SMs that the other leaves) the records of
+// that one join where an item ends. (Two kernels side by side on parts of the SMs, with all records
+// joined by the merge kernel, took 77 to 94 us instead of 73 at 130 sequences, the merge 12 of them.)
+//
+// Teams of 1, 2, 4 or 8 warps work by themselves. By items: a team takes whole items; long ones go to
+// a block or a cluster of up to 8 blocks that share out the item's steps and join their results
+// through distributed shared memory: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i. One launch, no
+// workspace. By steps: the flat space of (item, step) is cut into equal ranges, one per team, so that
+// items of any number and lengths fill the GPU evenly; an item that several teams share leaves one
+// record per team in global memory, which the merge kernel joins in the same way.
 #include <math_constants.h>
 #include <string.h>
 
@@ -271,17 +274,20 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
         else asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / T), "r"(32 * T) : "memory");
     };
     Walk w;
+    unsigned from, to;
     bool have;
+    const unsigned my_team = (blockIdx.x / (unsigned)parts) * (EX_WARPS / T) + warp / T;
     if (a.by_items) {
-        const unsigned team = (blockIdx.x / (unsigned)parts) * (EX_WARPS / T) + warp / T;
-        const unsigned from = team * a.share + min(team, a.extra);
-        have = w.begin(a, from, min(a.items, from + a.share + (team < a.extra ? 1u : 0u)), rs, rank,
-                       parts);
+        from = my_team * a.share + min(my_team, a.extra);
+        to = min(a.items, from + a.share + (my_team < a.extra ? 1u : 0u));
+        have = w.begin(a, from, to, rs, rank, parts);
     } else {
         const unsigned length = ex_length(a, a.B, rs);
-        const unsigned per = (length + a.grid - 1) / a.grid, from = blockIdx.x * per;
+        const unsigned per = (length + a.teams - 1) / a.teams;
+        from = my_team * per;
+        to = min(length, from + per);
         have = from < length;
-        if (have) w.begin_steps(a, from, min(length, from + per), rs);
+        if (have) w.begin_steps(a, from, to, rs);
     }
     bool late = false;                               // a wait hit its bound
     if (have) {
@@ -347,6 +353,27 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
         };
         const int tok = g / a.G, head = g - tok * a.G;
 
+        // a warp per query row, four channels per lane
+        auto write = [&](const Item &it, int r, const float4 &y, float L) {
+            const int tk = it.i0 + r / a.G, hd = r % a.G;
+            if (r / a.G >= ex_tpt(a.G) || tk >= it.i1) return;
+            const float inv = inverse(L);
+            char *op = a.out + it.b * a.o_seq + (it.h * a.G + hd) * a.o_head + tk * a.o_tok;
+            if constexpr (F32IO)
+                *reinterpret_cast<float4 *>(op + lane * 16) =
+                    make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+            else
+                *reinterpret_cast<uint2 *>(op + lane * 8) =
+                    make_uint2(pack(y.x * inv, y.y * inv), pack(y.z * inv, y.w * inv));
+        };
+        auto put = [&](int slot, int r, float M, float L, const float4 &y) {
+            float *rec = a.rec + (long long)slot * EX_REC;
+            if (lane == 0) {
+                rec[r] = M;
+                rec[EX_QROWS + r] = L;
+            }
+            *reinterpret_cast<float4 *>(rec + 2 * EX_QROWS + r * EX_D + lane * 4) = y;
+        };
         while (have) {
             const Item it = w.it;
             const int ti = it.i0 + tok;
@@ -403,6 +430,45 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
 
             // ---- the team's part of the item is complete: join its warps ------------------------
             const float l = x8.sum();
+            const bool whole = a.by_items || (w.s0 == 0 && w.s1 == w.S);
+            const bool finish = a.by_items || (whole && !MASS && !a.shared_here && !a.nsp);
+            // A part of an item leaves a record: the team's, 0 where the item began before it and 1
+            // where it goes on behind it; or the item's, where other records join it.
+            int slot = 2 * (int)my_team + (w.s0 == 0 ? 1 : 0);
+            if (whole) {
+                const int RT = ex_shared_span(a, rs).RT;
+                slot = 2 * a.teams + (it.b < 0 ? it.h * RT + it.rt : a.H * RT + it.b * a.H + it.h);
+            }
+            if (!MASS && T == 1 && !(finish && a.nsp)) {
+                // one warp: straight from its registers
+                if (live && g < a.G * ex_tpt(a.G)) {
+                    if (finish) {
+                        const float inv = inverse(l);
+                        char *op = a.out + it.b * a.o_seq + (it.h * a.G + head) * a.o_head + ti * a.o_tok;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int d = 8 * i + 2 * t;
+                            if constexpr (F32IO)
+                                *reinterpret_cast<float2 *>(op + d * 4) =
+                                    make_float2(x8.o[i].x * inv, x8.o[i].y * inv);
+                            else
+                                *reinterpret_cast<uint32_t *>(op + d * 2) =
+                                    pack(x8.o[i].x * inv, x8.o[i].y * inv);
+                        }
+                    } else {
+                        float *rec = a.rec + (long long)slot * EX_REC;
+                        if (t == 0) {
+                            rec[g] = x8.m;
+                            rec[EX_QROWS + g] = l;
+                        }
+                        rec += 2 * EX_QROWS + g * EX_D + 2 * t;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) *reinterpret_cast<float2 *>(rec + 8 * i) = x8.o[i];
+                    }
+                }
+                have = w.next(a, rs, rank, parts);
+                continue;
+            }
             float *mine = red + (warp * EX_QROWS + g) * RED + 2 * t;
 #pragma unroll
             for (int i = 0; i < 16; ++i) *reinterpret_cast<float2 *>(mine + 8 * i) = x8.o[i];
@@ -411,39 +477,17 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                 red_l[warp * EX_QROWS + g] = l;
             }
             team_sync();
-            // A part of an item leaves a record: the block's, 0 where the item began before it and 1
-            // where it goes on behind it; or the item's, where other records join it.
-            const bool whole = a.by_items || (w.s0 == 0 && w.s1 == w.S);
-            const bool finish = a.by_items || (whole && !MASS && !a.shared_here);
-            int slot = 2 * blockIdx.x + (w.s0 == 0 ? 1 : 0);
-            if (!finish && whole) {
-                const int RT = ex_shared_span(a, rs).RT;
-                slot = 2 * a.grid + (it.b < 0 ? it.h * RT + it.rt : a.H * RT + it.b * a.H + it.h);
-            }
-            // a warp per query row, four channels per lane
-            auto write = [&](int r, const float4 &y, float L) {
-                const int tk = it.i0 + r / a.G, hd = r % a.G;
-                if (r / a.G >= ex_tpt(a.G) || tk >= it.i1) return;
-                const float inv = inverse(L);
-                char *op = a.out + it.b * a.o_seq + (it.h * a.G + hd) * a.o_head + tk * a.o_tok;
-                if constexpr (F32IO)
-                    *reinterpret_cast<float4 *>(op + lane * 16) =
-                        make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-                else
-                    *reinterpret_cast<uint2 *>(op + lane * 8) =
-                        make_uint2(pack(y.x * inv, y.y * inv), pack(y.z * inv, y.w * inv));
-            };
-            const int nsp = finish && rank == 0 ? a.nsp : 0;   // (one block of a cluster adds them)
+            const int used = (it.i1 - it.i0) * a.G;
+            const int nsp = !MASS && finish && rank == 0 ? a.nsp : 0;   // (one block of a cluster)
             if (nsp) asm volatile("griddepcontrol.wait;" ::: "memory");
-            const int used = ex_tpt(a.G) * a.G;
-            for (int r = tw; r < (finish ? used : EX_QROWS); r += T) {
+            for (int r = tw; r < used; r += T) {
                 float M = -CUDART_INF_F, mx[EX_WARPS];
 #pragma unroll
                 for (int x = 0; x < EX_WARPS; ++x) {
                     mx[x] = x < T ? red_m[(team0 + x) * EX_QROWS + r] : -CUDART_INF_F;
                     M = fmaxf(M, mx[x]);
                 }
-                // the tile kernel's records of this row: lane x has record x
+                // the prefix's records of this row: lane x has record x
                 float pm_ = -CUDART_INF_F, pl_ = 0.f;
                 const long long pre = ((long long)it.h * a.nsp * a.B + it.b) * a.G + r;
                 const long long pre_st = (long long)a.B * a.G;
@@ -493,7 +537,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                     }
                 }
                 if (finish && parts == 1) {
-                    write(r, y, L);
+                    write(it, r, y, L);
                     if (MASS && lane == 0) {
                         // (reference, sum) of the row for the weights below
                         red_m[team0 * EX_QROWS + r] = ref;
@@ -507,12 +551,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                         sum_l[r] = L;
                     }
                 } else {
-                    float *rec = a.rec + (long long)slot * EX_REC;
-                    if (lane == 0) {
-                        rec[r] = M;
-                        rec[EX_QROWS + r] = L;
-                    }
-                    *reinterpret_cast<float4 *>(rec + 2 * EX_QROWS + r * EX_D + lane * 4) = y;
+                    put(slot, r, M, L, y);
                 }
             }
             if (parts > 1) {
@@ -552,7 +591,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                             y.z += f * v[x].z;
                             y.w += f * v[x].w;
                         }
-                        write(r, y, L);
+                        write(it, r, y, L);
                     }
                     if (MASS && warp < used) {
                         // every block: (reference, sum) of all rows; warp = row, lane x = block x
@@ -646,13 +685,13 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
 // own records with its rows of the prefix's). The blocks after them add the weights to `mass`.
 constexpr int MERGE_T = 256;
 constexpr int MASS_ROWS = 4 * MERGE_T;      // rows per mass block
+constexpr int MERGE_CHUNK = 256;            // records whose weights are at hand
 
 template <bool F32ROWS, bool F32IO, bool MASS>
 __global__ void __launch_bounds__(MERGE_T)
 exact_merge_kernel(const __grid_constant__ ExactArgs a, int rt_max, int mass_blocks) {
-    constexpr int RS = ex_step_rows(F32ROWS);
-    __shared__ float wgt[EX_QROWS][EX_MAXREC];
-    __shared__ int slot_of[EX_MAXREC];
+    const int RS = ex_warp_rows(F32ROWS) * a.team;
+    __shared__ float wgt[EX_QROWS][MERGE_CHUNK];
     __shared__ float row_m[EX_QROWS], row_l[EX_QROWS];
     __shared__ __align__(16) float part[MERGE_T * 4];
     const int n_items = a.B * a.H * rt_max;
@@ -674,11 +713,11 @@ exact_merge_kernel(const __grid_constant__ ExactArgs a, int rt_max, int mass_blo
     const ExactSpan sp = ex_seq_span(a, n, ql, RS), sh = ex_shared_span(a, RS);
     if (rt >= sp.RT || (mass_block && chunk * MASS_ROWS >= n)) return;
     const unsigned length = ex_length(a, a.B, RS);
-    const unsigned per = (length + a.grid - 1) / a.grid;
+    const unsigned per = (length + a.teams - 1) / a.teams;
     const unsigned first = ex_length(a, b, RS) + ((unsigned)h * sp.RT + rt) * sp.S;
     const int own_c0 = (int)(first / per), own_c1 = (int)((first + sp.S - 1) / per);
     const int n_own = own_c1 - own_c0 + 1;
-    if (!MASS && !a.shared_here && n_own == 1) return;   // the split kernel wrote it
+    if (!MASS && !a.shared_here && !a.nsp && n_own == 1) return;   // the split kernel wrote it
     // shared prefix: tile and row of this sequence
     int n_sh = 0, sh_c0 = 0;
     const int sh_rt = b / tpt, sh_row = (b - sh_rt * tpt) * a.G;
@@ -688,52 +727,46 @@ exact_merge_kernel(const __grid_constant__ ExactArgs a, int rt_max, int mass_blo
         n_sh = (int)((f + sh.S - 1) / per) - sh_c0 + 1;
     }
     const int nrec = n_own + n_sh + a.nsp;
-    const int whole0 = 2 * a.grid;
-    for (int i = threadIdx.x; i < n_own + n_sh; i += MERGE_T) {
+    const int whole0 = 2 * a.teams;
+    auto slot_of = [&](int i) {
         if (i < n_own)
-            slot_of[i] = n_own == 1 ? whole0 + a.H * sh.RT + b * a.H + h
-                                    : 2 * (own_c0 + i) + (i == 0 ? 1 : 0);
-        else
-            slot_of[i] = n_sh == 1 ? whole0 + h * sh.RT + sh_rt
-                                   : 2 * (sh_c0 + i - n_own) + (i == n_own ? 1 : 0);
-    }
+            return n_own == 1 ? whole0 + a.H * sh.RT + b * a.H + h
+                              : 2 * (own_c0 + i) + (i == 0 ? 1 : 0);
+        return n_sh == 1 ? whole0 + h * sh.RT + sh_rt
+                         : 2 * (sh_c0 + i - n_own) + (i == n_own ? 1 : 0);
+    };
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    __syncthreads();
     const int rows = min(tpt, ql - rt * tpt) * a.G;              // live rows of the tile
     auto ml = [&](int i, int r, float &m_, float &l_) {
         if (i < n_own + n_sh) {
-            const float *rec = a.rec + (long long)slot_of[i] * EX_REC;
+            const float *rec = a.rec + (long long)slot_of(i) * EX_REC;
             const int rr = i < n_own ? r : sh_row + r;
             m_ = rec[rr];
             l_ = rec[EX_QROWS + rr];
         } else {
-            const float *x = a.pre_ml + 2 * (((long long)h * a.nsp + (i - n_own - n_sh)) * a.B * a.G +
-                                             (long long)b * a.G + r);
-            m_ = x[0];
-            l_ = x[1];
+            const float2 x = *reinterpret_cast<const float2 *>(
+                a.pre_ml + 2 * (((long long)h * a.nsp + (i - n_own - n_sh)) * a.B * a.G +
+                                (long long)b * a.G + r));
+            m_ = x.x;
+            l_ = x.y;
         }
     };
-    // a warp per row: M = max m_i, weights 2^(m_i - M), L = sum of weight x l_i
+    // a warp per row: M = max m_i, L = sum of 2^(m_i - M) l_i
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp < rows) {
-        float M = -CUDART_INF_F;
+        float M = -CUDART_INF_F, L = 0.f;
         for (int i = lane; i < nrec; i += 32) {
             float m_, l_;
             ml(i, warp, m_, l_);
-            wgt[warp][i] = m_;
-            M = fmaxf(M, m_);
+            const float top = fmaxf(M, m_);
+            if (top > -CUDART_INF_F) L = L * ex2(M - top) + l_ * ex2(m_ - top);
+            M = top;
         }
+        float top = M;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const float ref = M == -CUDART_INF_F ? 0.f : M;
-        float L = 0.f;
-        for (int i = lane; i < nrec; i += 32) {
-            float m_, l_;
-            ml(i, warp, m_, l_);
-            const float f = ex2(wgt[warp][i] - ref);
-            wgt[warp][i] = f;
-            L += f * l_;
-        }
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float ref = top == -CUDART_INF_F ? 0.f : top;
+        L *= ex2(M - ref);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
         if (lane == 0) {
@@ -772,22 +805,33 @@ exact_merge_kernel(const __grid_constant__ ExactArgs a, int rt_max, int mass_blo
     const int y = threadIdx.x / lanes, e = threadIdx.x - y * lanes;
     const int r = e / (EX_D / 4), d = (e % (EX_D / 4)) * 4;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (y < reps) {
+    for (int i0 = 0; i0 < nrec; i0 += MERGE_CHUNK) {
+        const int i1 = min(nrec, i0 + MERGE_CHUNK);
+        if (i0 > 0) __syncthreads();
+        if (warp < rows)
+            for (int i = i0 + lane; i < i1; i += 32) {
+                float m_, l_;
+                ml(i, warp, m_, l_);
+                wgt[warp][i - i0] = ex2(m_ - row_m[warp]);
+            }
+        __syncthreads();
+        if (y < reps) {
 #pragma unroll 4
-        for (int i = y; i < nrec; i += reps) {
-            const float *src;
-            if (i < n_own + n_sh)
-                src = a.rec + (long long)slot_of[i] * EX_REC + 2 * EX_QROWS +
-                      (i < n_own ? r : sh_row + r) * EX_D + d;
-            else
-                src = a.pre_o + (((long long)h * a.nsp + (i - n_own - n_sh)) * a.B * a.G +
-                                 (long long)b * a.G + r) * EX_D + d;
-            const float4 v = *reinterpret_cast<const float4 *>(src);
-            const float f = wgt[r][i];
-            acc.x += f * v.x;
-            acc.y += f * v.y;
-            acc.z += f * v.z;
-            acc.w += f * v.w;
+            for (int i = i0 + y; i < i1; i += reps) {
+                const float *src;
+                if (i < n_own + n_sh)
+                    src = a.rec + (long long)slot_of(i) * EX_REC + 2 * EX_QROWS +
+                          (i < n_own ? r : sh_row + r) * EX_D + d;
+                else
+                    src = a.pre_o + (((long long)h * a.nsp + (i - n_own - n_sh)) * a.B * a.G +
+                                     (long long)b * a.G + r) * EX_D + d;
+                const float4 v = *reinterpret_cast<const float4 *>(src);
+                const float f = wgt[r][i - i0];
+                acc.x += f * v.x;
+                acc.y += f * v.y;
+                acc.z += f * v.z;
+                acc.w += f * v.w;
+            }
         }
     }
     *reinterpret_cast<float4 *>(part + threadIdx.x * 4) = acc;

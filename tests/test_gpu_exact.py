@@ -79,6 +79,8 @@ WINDOW_CASES = [
     (2, 1, 8, 333, 200, 77, 40, "f32", "f32", [333, 150], [200, 150], False),
     (1, 1, 5, 3000, 30, 1 << 24, 0, "f32", "bf16", None, None, False),
     (1, 1, 4, 5000, 9, 4000, 100, "bf16", "bf16", None, None, False),
+    (70, 8, 2, 700, 1, 300, 40, "bf16", "bf16", list(range(1, 701, 10)), None, False),
+    (160, 2, 4, 90, 2, 1000, 0, "f32", "bf16", [90] * 160, [2, 0] * 80, True),
 ]
 
 
@@ -187,7 +189,8 @@ PREFIX_CASES = [
     (16, 1, 8, 2100, 5, "bf16", "bf16", None), (300, 1, 2, 128, 1, "bf16", "bf16", None),
     (5, 2, 3, 4000, 33, "bf16", "bf16", [33, 0, 2, 3, 4]),
     (9, 1, 8, 500, 1500, "bf16", "bf16", None), (40, 1, 4, 1100, 600, "f32", "bf16", None),
-    (150, 1, 2, 257, 40, "f32", "f32", None), (20, 2, 4, 900, 300, "f32", "f32", [300, 1] * 10),
+    (150, 1, 2, 257, 40, "f32", "f32", None), (40, 1, 4, 300, 60000, "bf16", "bf16",
+                                               [60000] + [0] * 38 + [7]), (20, 2, 4, 900, 300, "f32", "f32", [300, 1] * 10),
 ]
 
 
