@@ -182,6 +182,18 @@ bool rows_map(CUtensorMap *map, const void *base, int dtype, int rows, int heads
     return encode(map, dtype, 5, base, dims, strides, box);
 }
 
+// The same rows as (channels, row, kv-head, sequence), boxes of 64 channels of 16 bf16 rows.
+bool rows16_map(CUtensorMap *map, const iskv_exact_rows *r, const void *base) {
+    auto ext = [](long long st, int n) { return (cuuint64_t)(n > 1 && st == 0 ? 1 : n); };
+    auto str = [](long long st, int n) { return (cuuint64_t)(n > 1 && st ? st * 2 : 256); };
+    const cuuint64_t dims[4] = {EX_D, (cuuint64_t)r->rows, ext(r->head_stride, r->n_kv_heads),
+                                ext(r->seq_stride, r->batch)};
+    const cuuint64_t strides[3] = {str(r->row_stride, r->rows), str(r->head_stride, r->n_kv_heads),
+                                   str(r->seq_stride, r->batch)};
+    const cuuint32_t box[4] = {64, 16, 1, 1};
+    return encode(map, ISKV_BF16, 4, base, dims, strides, box);
+}
+
 bool own_maps(CUtensorMap *k, CUtensorMap *v, const iskv_exact_rows *r, int box_rows) {
     if (r->rows == 0) return true;                   // never read
     return rows_map(k, r->k, r->dtype, r->rows, r->n_kv_heads, r->batch, r->row_stride,
@@ -240,7 +252,7 @@ TilePlan window_plan(const iskv_exact_rows *r, const iskv_exact_queries *q, int 
                      bool tile, int sms) {
     const int G = q->n_q_heads / r->n_kv_heads;
     // rows that a pair of tiles sees at most
-    const long long near = (long long)window + sinks + 2 * (TILE_ROWS / G);
+    const long long near = (long long)window + sinks + 15 + 2 * (TILE_ROWS / G);
     return tile_plan(r->batch * r->n_kv_heads, q->m, G, near < r->rows ? near : r->rows, tile, sms);
 }
 
@@ -389,16 +401,18 @@ extern "C" int iskv_window_attn(const iskv_exact_rows *r, const iskv_exact_queri
     a.sinks = sinks < r->rows ? sinks : r->rows;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool fr = r->dtype == ISKV_F32, fi = q->dtype == ISKV_F32;
-    CUtensorMap qm, km, vm;
+    TileMaps tm;
     TilePlan p = window_plan(r, q, window, sinks, all_bf16(r, q), a.grid);
-    if (p.tile && !query_map(&qm, a, false, p.tq))
+    if (p.tile && !query_map(&tm.q, a, false, p.tq))
         p = window_plan(r, q, window, sinks, false, a.grid);
     if (p.use) {
-        if (!own_maps(&km, &vm, r, p.tile ? TILE_ROWS : ex_warp_rows(fr))) return ISKV_ERR_CUDA;
+        if (!own_maps(&tm.k, &tm.v, r, p.tile ? TILE_ROWS : ex_warp_rows(fr)) ||
+            (p.tile && !(rows16_map(&tm.k16, r, r->k) && rows16_map(&tm.v16, r, r->v))))
+            return ISKV_ERR_CUDA;
         TileArgs t;
         tile_args(t, p, a, false, p.nsp > 1 ? static_cast<float *>(ws) : nullptr);
-        const int e = launched(p.tile ? launch_exact_tile(t, qm, km, vm, false, p.alternate, s)
-                                      : launch_exact_rows(t, km, vm, fr, fi, false, s));
+        const int e = launched(p.tile ? launch_exact_tile(t, tm, false, p.alternate, s)
+                                      : launch_exact_rows(t, tm.k, tm.v, fr, fi, false, s));
         if (e != ISKV_OK || p.nsp == 1) return e;
         return launched(launch_exact_tile_merge(t, fi, s));
     }
@@ -484,18 +498,18 @@ extern "C" int iskv_prefix_decode(const iskv_exact_rows *r, const iskv_exact_que
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool fr = r->dtype == ISKV_F32, fi = q->dtype == ISKV_F32;
     ExactMaps maps;
-    CUtensorMap qm, km, vm;
+    TileMaps tm;
     TilePlan plan = prefix_plan(r, q, p, all_bf16(r, q), a.grid);
-    if (plan.tile && !query_map(&qm, a, true, plan.tq)) plan = prefix_plan(r, q, p, false, a.grid);
+    if (plan.tile && !query_map(&tm.q, a, true, plan.tq)) plan = prefix_plan(r, q, p, false, a.grid);
     if (plan.use) {
-        if (!prefix_maps(&km, &vm, r, p, plan.tile ? TILE_ROWS : ex_warp_rows(fr)))
+        if (!prefix_maps(&tm.k, &tm.v, r, p, plan.tile ? TILE_ROWS : ex_warp_rows(fr)))
             return ISKV_ERR_CUDA;
         const int tpt = ex_tpt(a.G);
         const size_t at = record_bytes(a.grid, (long long)a.H * (a.B + (a.B + tpt - 1) / tpt));
         TileArgs t;
         tile_args(t, plan, a, true, reinterpret_cast<float *>(static_cast<char *>(ws) + at));
-        const int e = launched(plan.tile ? launch_exact_tile(t, qm, km, vm, true, plan.alternate, s)
-                                         : launch_exact_rows(t, km, vm, fr, fi, true, s));
+        const int e = launched(plan.tile ? launch_exact_tile(t, tm, true, plan.alternate, s)
+                                         : launch_exact_rows(t, tm.k, tm.v, fr, fi, true, s));
         if (e != ISKV_OK) return e;
         a.pre_ml = t.pre_ml;
         a.pre_o = t.pre_o;

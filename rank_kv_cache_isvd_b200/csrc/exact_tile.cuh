@@ -29,10 +29,14 @@ struct TileArgs {
     int sms;
 };
 
-// Maps of q (channels, q-heads, tokens, sequences) in boxes of 64 channels, and of the rows (64
-// channels, rows, halves, kv-heads, sequences) in boxes of 128 whole rows.
-cudaError_t launch_exact_tile(const TileArgs &a, const CUtensorMap &q, const CUtensorMap &k,
-                              const CUtensorMap &v, bool prefix, bool alternate, cudaStream_t s);
+// Maps of q (channels, q-heads, tokens, sequences) in boxes of 64 channels; of the rows (64 channels,
+// rows, halves, kv-heads, sequences) in boxes of 128 whole rows, and (channels, rows, kv-heads,
+// sequences) in boxes of 64 channels of 16 rows (not prefix).
+struct TileMaps {
+    CUtensorMap q, k, v, k16, v16;
+};
+cudaError_t launch_exact_tile(const TileArgs &a, const TileMaps &maps, bool prefix, bool alternate,
+                              cudaStream_t s);
 
 // Maps of the rows in boxes of ex_warp_rows() whole rows.
 cudaError_t launch_exact_rows(const TileArgs &a, const CUtensorMap &k, const CUtensorMap &v,
