@@ -378,8 +378,8 @@ typedef struct {
  * sees the rows j <= p with j < sinks or j > p - window (window >= lens: causal attention). From
  * a whole prompt (m = rows) to single tokens (m = 1). Outputs of tokens i >= q_lens[b] are not
  * written. A token's own row has to be in the cache before the call.
- * Where tokens see different rows of a call, a row that is not finite may reach every token
- * within 64 positions of one that sees it.
+ * Where tokens see different rows of a call, a value that is not finite may reach every token
+ * within 256 positions of one that sees it; it reaches no other.
  * Errors: ISKV_ERR_INVALID_ARG, ISKV_ERR_UNSUPPORTED, ISKV_ERR_CAPACITY (workspace too small),
  *         ISKV_ERR_CUDA.
  */

@@ -83,7 +83,7 @@ int check_queries(const iskv_exact_rows *r, const iskv_exact_queries *q) {
     // (tile, step) pairs are counted in 32 bits
     const long long tiles = (q->m + ex_tpt(q->n_q_heads / r->n_kv_heads) - 1) /
                             ex_tpt(q->n_q_heads / r->n_kv_heads);
-    if ((long long)r->batch * r->n_kv_heads * tiles * (r->rows / 128 + 2) > 0x7fffffffLL)
+    if ((long long)r->batch * r->n_kv_heads * tiles * (r->rows / 16 + 3) > 0x7fffffffLL)
         return ISKV_ERR_UNSUPPORTED;
     return ISKV_OK;
 }

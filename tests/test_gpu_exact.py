@@ -121,6 +121,24 @@ def test_window_never_reads_what_no_token_sees(io, rt):
     _check_window(k, v, q, out, lens, [1, 1], window, sinks, T[io], out.clone())
 
 
+@pytest.mark.parametrize("G,io", [(4, "bf16"), (1, "bf16"), (4, "f32")])
+def test_values_that_are_not_finite_stay_near_their_window(G, io):
+    """One NaN among the values of a prompt: tokens more than 256 positions away from all that see it
+    come out as if it were not there."""
+    g = _gen(12)
+    n, window, at = 1400, 100, 600
+    k, v = _kv(g, 1, 1, n, "bf16")
+    q = torch.randn((1, G, n, D), generator=g, device="cuda").to(T[io])
+    v[0, 0, at] = float("nan")
+    out = _cache(k, v).window_attn(q, window=window)[0].double().cpu()
+    far = [i for i in range(n) if i < at - 256 or i >= at + window + 256]
+    see = visible(n, n, n, window, 0)[far]
+    for a in range(G):
+        ref = Attended(q[0, a, far], k[0, 0], v[0, 0], see)
+        assert ((out[a, far] - ref.o).abs() <= out_bound(ref, T[io], T[io])).all()
+    assert torch.isnan(out[:, at:at + window]).all()
+
+
 @pytest.mark.parametrize("sharp", [1.0, 12.0])
 def test_window_prompt_of_many_blocks(sharp):
     """A prompt of several thousand tokens, on a sample of its tokens; sharp: logits of about 50."""
@@ -342,6 +360,50 @@ def test_calls_on_another_stream_and_in_graphs():
     torch.cuda.synchronize()
     for o, mo in zip(outs, masses):
         assert torch.equal(o, want) and torch.equal(mo, want_m)
+
+
+def test_every_call_captured_without_a_first_one():
+    """All calls in one graph of a fresh object (its workspace and plans are made while capturing),
+    replayed on new contents: the same bits as eager calls."""
+    g = _gen(13)
+    B, H, G, n, P, budget = 20, 2, 4, 400, 300, 350
+    k, v = _kv(g, B, H, n, "bf16")
+    pk, pv = (x[0] for x in _kv(g, 1, H, P, "bf16"))
+    q = torch.randn((B, H * G, 30, D), generator=g, device="cuda").bfloat16()
+    q1 = torch.randn((B, H * G, D), generator=g, device="cuda")
+    mass = torch.rand((B, H, n), generator=g, device="cuda")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda").expand(B, H, n).contiguous()
+    lens = _i32([n - b for b in range(B)])
+    start = [x.clone() for x in (k, v, mass, pos, lens, q, q1)]
+
+    def calls(c):
+        a = c.window_attn(q, window=64, sinks=3)
+        b = c.mass_decode(q1, mass)[0]
+        p = c.prefix_decode(q1, pk, pv)
+        p2 = c.prefix_decode(q1.bfloat16(), pk, pv)
+        c.evict(mass, pos, budget=budget, recent=16, sinks=2)
+        return a, b, p, p2
+
+    c = _cache(k, v, lens)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls(c)
+    for scale in (1.0, -0.5):
+        for x, y in zip((k, v, mass, pos, lens, q, q1), start):
+            x.copy_(y)
+        q.mul_(scale)
+        graph.replay()
+        torch.cuda.synchronize()
+        seen = [x.clone() for x in (*got, k, v, mass, pos, lens)]
+        for x, y in zip((k, v, mass, pos, lens, q, q1), start):
+            x.copy_(y)
+        q.mul_(scale)
+        eager = calls(_cache(k, v, lens))
+        torch.cuda.synchronize()
+        for x, y in zip(seen, (*eager, k, v, mass, pos, lens)):
+            assert torch.equal(x, y)
+        assert lens.tolist() == [min(n - b, budget) for b in range(B)]
 
 
 def test_prompt_then_decode_with_eviction():
