@@ -480,33 +480,18 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
             const int used = (it.i1 - it.i0) * a.G;
             const int nsp = !MASS && finish && rank == 0 ? a.nsp : 0;   // (one block of a cluster)
             if (nsp) asm volatile("griddepcontrol.wait;" ::: "memory");
-            for (int r = tw; r < used; r += T) {
-                float M = -CUDART_INF_F, mx[EX_WARPS];
+            // Joins the team's parts of row r, and (p_m, p_l, p_y) where there is a prefix.
+            auto join = [&](int r, float p_m, float p_l, const float4 &p_y) {
+                float M = p_m, mx[EX_WARPS];
 #pragma unroll
                 for (int x = 0; x < EX_WARPS; ++x) {
                     mx[x] = x < T ? red_m[(team0 + x) * EX_QROWS + r] : -CUDART_INF_F;
                     M = fmaxf(M, mx[x]);
                 }
-                // the prefix's records of this row: lane x has record x
-                float pm_ = -CUDART_INF_F, pl_ = 0.f;
-                const long long pre = ((long long)it.h * a.nsp * a.B + it.b) * a.G + r;
-                const long long pre_st = (long long)a.B * a.G;
-                if (nsp) {
-                    if (lane < nsp) {
-                        const float2 ml = __ldcg(
-                            reinterpret_cast<const float2 *>(a.pre_ml + 2 * (pre + lane * pre_st)));
-                        pm_ = ml.x;
-                        pl_ = ml.y;
-                    }
-                    float top = pm_;
-#pragma unroll
-                    for (int x = 16; x > 0; x >>= 1)
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                    M = fmaxf(M, top);
-                }
                 const float ref = M == -CUDART_INF_F ? 0.f : M;
-                float L = 0.f;
-                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                const float f0 = ex2(p_m - ref);
+                float L = f0 * p_l;
+                float4 y = make_float4(f0 * p_y.x, f0 * p_y.y, f0 * p_y.z, f0 * p_y.w);
 #pragma unroll
                 for (int x = 0; x < EX_WARPS; ++x) {
                     if (x >= T) break;
@@ -518,23 +503,6 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                     y.y += f * v.y;
                     y.z += f * v.z;
                     y.w += f * v.w;
-                }
-                if (nsp) {
-                    const float f = ex2(pm_ - ref);
-                    float add = f * pl_;
-#pragma unroll
-                    for (int x = 16; x > 0; x >>= 1) add += __shfl_xor_sync(0xffffffffu, add, x);
-                    L += add;
-#pragma unroll 6
-                    for (int x = 0; x < nsp; ++x) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(
-                            a.pre_o + (pre + x * pre_st) * EX_D + lane * 4));
-                        const float fx = __shfl_sync(0xffffffffu, f, x);
-                        y.x += fx * v.x;
-                        y.y += fx * v.y;
-                        y.z += fx * v.z;
-                        y.w += fx * v.w;
-                    }
                 }
                 if (finish && parts == 1) {
                     write(it, r, y, L);
@@ -553,6 +521,74 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                 } else {
                     put(slot, r, M, L, y);
                 }
+            };
+            if (!MASS && nsp) {
+                // the prefix's records of K of the warp's rows, all loads of a turn in flight together
+                auto with_prefix = [&](auto k_, auto u_) {
+                    constexpr int K = decltype(k_)::value, U = decltype(u_)::value;
+                    for (int r0 = tw; r0 < used; r0 += K * T) {
+                        const long long pre = ((long long)it.h * a.nsp * a.B + it.b) * a.G + r0;
+                        const long long pre_st = (long long)a.B * a.G;
+                        float pm_[K], pl_[K], f[K];
+                        float4 y[K];
+#pragma unroll
+                        for (int k = 0; k < K; ++k) {        // lane x: record x
+                            pm_[k] = -CUDART_INF_F;
+                            pl_[k] = 0.f;
+                            if (lane < nsp && r0 + k * T < used) {
+                                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(
+                                    a.pre_ml + 2 * (pre + k * T + lane * pre_st)));
+                                pm_[k] = ml.x;
+                                pl_[k] = ml.y;
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < K; ++k) {
+                            float top = pm_[k];
+#pragma unroll
+                            for (int x = 16; x > 0; x >>= 1)
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                            f[k] = ex2(pm_[k] - (top == -CUDART_INF_F ? 0.f : top));
+                            float add = f[k] * pl_[k];
+#pragma unroll
+                            for (int x = 16; x > 0; x >>= 1)
+                                add += __shfl_xor_sync(0xffffffffu, add, x);
+                            pm_[k] = top;
+                            pl_[k] = add;
+                            y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+                        for (int x0 = 0; x0 < nsp; x0 += U) {
+                            float4 v[U][K];
+#pragma unroll
+                            for (int u = 0; u < U; ++u)
+#pragma unroll
+                                for (int k = 0; k < K; ++k)
+                                    v[u][k] = x0 + u < nsp && r0 + k * T < used
+                                                  ? __ldcg(reinterpret_cast<const float4 *>(
+                                                        a.pre_o + (pre + k * T + (x0 + u) * pre_st) * EX_D +
+                                                        lane * 4))
+                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                            for (int u = 0; u < U; ++u)
+#pragma unroll
+                                for (int k = 0; k < K; ++k) {
+                                    const float fx = __shfl_sync(0xffffffffu, f[k], (x0 + u) & 31);
+                                    y[k].x += fx * v[u][k].x;
+                                    y[k].y += fx * v[u][k].y;
+                                    y[k].z += fx * v[u][k].z;
+                                    y[k].w += fx * v[u][k].w;
+                                }
+                        }
+#pragma unroll
+                        for (int k = 0; k < K; ++k)
+                            if (r0 + k * T < used) join(r0 + k * T, pm_[k], pl_[k], y[k]);
+                    }
+                };
+                if (used <= T) with_prefix(std::integral_constant<int, 1>{}, std::integral_constant<int, 9>{});
+                else with_prefix(std::integral_constant<int, 4>{}, std::integral_constant<int, 3>{});
+            } else {
+                for (int r = tw; r < used; r += T)
+                    join(r, -CUDART_INF_F, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
             }
             if (parts > 1) {
                 // row r of the item is finished by block r mod parts; all loads are issued at once

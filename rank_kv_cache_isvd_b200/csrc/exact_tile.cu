@@ -559,31 +559,33 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ Ti
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
         }
-        float *half = reinterpret_cast<float *>(ring);  // [channel][row], then m and l: free by now
+        float *half = reinterpret_cast<float *>(ring);  // free by now; see `give`
+        constexpr int CG = ALT ? 2 : 4;                 // quarters of the channels that a group puts out
+        const int c0 = ALT && i == 1 ? 2 : 0;
         if (ALT) {
-            // the groups' shares of the blocks join: the second leaves its part in shared memory
-            if (i == 1) {
+            // The groups' shares of the blocks join, each group for half of the channels: it gives
+            // the other half, [channel][row], and both m and l to the other.
+            float *give = half + (1 - i) * 64 * TILE_ROWS;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float o[32];
-                    if (mine > 0) {
-                        tmem_ld32(o_t + c * 32, o);
-                        tmem_wait_ld();
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        half[(c * 32 + e) * TILE_ROWS + row] = mine > 0 ? o[e] : 0.f;
+            for (int c = 0; c < 2; ++c) {
+                float o[32];
+                if (mine > 0) {
+                    tmem_ld32(o_t + (2 - c0 + c) * 32, o);
+                    tmem_wait_ld();
                 }
-                half[TILE_ROWS * EX_D + row] = m;
-                half[TILE_ROWS * EX_D + TILE_ROWS + row] = l;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) give[(c * 32 + e) * TILE_ROWS + row] = mine > 0 ? o[e] : 0.f;
             }
+            half[(128 + 2 * i) * TILE_ROWS + row] = m;
+            half[(129 + 2 * i) * TILE_ROWS + row] = l;
             asm volatile("bar.sync 1, 256;" ::: "memory");
         }
-        if (ok && !(ALT && i == 1)) {
+        if (ok) {
             const bool record = PREFIX || a.nsp > 1;
             float f0 = 1.f, f1 = 0.f, all_m = m, all_l = l;
             if (ALT) {
-                const float m1 = half[TILE_ROWS * EX_D + row], l1 = half[TILE_ROWS * EX_D + TILE_ROWS + row];
+                const float m1 = half[(130 - 2 * i) * TILE_ROWS + row];
+                const float l1 = half[(131 - 2 * i) * TILE_ROWS + row];
                 all_m = fmaxf(m, m1);
                 const float ref = all_m == -CUDART_INF_F ? 0.f : all_m;
                 f0 = ex2(m - ref);
@@ -599,12 +601,13 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ Ti
                               : a.out + w.b * a.o_seq + (long long)(w.h * a.G + gq) * a.o_head +
                                     tok * a.o_tok;
             if (!live) to = nullptr;
-            else if (record)
+            else if (record && c0 == 0)
                 *reinterpret_cast<float2 *>(a.pre_ml + 2 * at) = make_float2(all_m, all_l);
-            uint8_t *stage = ring + (ALT ? 3 * BLOCK_BYTES : 0) + (ALT ? warp & 3 : warp - 4) * 8192;
+            uint8_t *stage = ring + (ALT ? 3 * BLOCK_BYTES : 0) + (warp - 4) * 4096;
             // two halves of 64 channels (record: four of 32), 128 bytes of a row each
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int x = 0; x < CG; ++x) {
+                const int c = c0 + x;
                 float o[32];
                 if (mine > 0) {
                     tmem_ld32(o_t + c * 32, o);
@@ -616,7 +619,7 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ Ti
                 if (ALT) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        o[e] = f0 * o[e] + f1 * half[(c * 32 + e) * TILE_ROWS + row];
+                        o[e] = f0 * o[e] + f1 * half[(i * 64 + x * 32 + e) * TILE_ROWS + row];
                 }
                 if (record) {
 #pragma unroll
@@ -627,12 +630,12 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ Ti
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         *reinterpret_cast<uint4 *>(stage + lane * 128 +
-                                                   (((4 * (c & 1) + e) ^ (lane & 7)) * 16)) =
+                                                   (((4 * (x & 1) + e) ^ (lane & 7)) * 16)) =
                             make_uint4(pack(o[8 * e] * inv, o[8 * e + 1] * inv),
                                        pack(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
                                        pack(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
                                        pack(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-                    if (!(c & 1)) continue;
+                    if (!(x & 1)) continue;
                 }
                 __syncwarp();
                 const int part = record ? c : c >> 1;
