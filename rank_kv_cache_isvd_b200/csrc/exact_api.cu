@@ -287,7 +287,6 @@ void tile_args(TileArgs &t, const TilePlan &p, const ExactArgs &a, bool prefix, 
     t.o_head = a.o_head;
     t.o_tok = a.o_tok;
     t.scale_log2 = a.scale_log2;
-    t.sms = a.grid;
     t.pre_ml = records;
     if (records)
         t.pre_o = reinterpret_cast<float *>(

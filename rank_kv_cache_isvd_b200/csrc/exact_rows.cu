@@ -5,8 +5,9 @@
 // tf32 products (exact_warp.cuh): 64 mma.sync per 32 keys and 8 rows, the bound of this kernel at
 // 145 TFLOP/s of float32 work. A CTA takes 64 query rows, 8 per warp, and all warps share one ring
 // of key and value units in shared memory. (The split kernel, which gives each tile of 8 rows its own
-// copy of the rows, was bound by L2 here: 950 us against 250 us at 130 x 8 rows over a prefix of
-// 16384.) As in the tile kernel a CTA does a split of the rows' steps where CTAs are few.
+// copy of the rows, was bound by L2 here: 950 us against 425 us at 94 x 4 queries of 8 kv-heads over
+// 7264 shared rows.) The same products reach 73 TFLOP/s (130 x 8 queries over 16384 shared rows:
+// 957 us); fetching and decoding instructions, then the splitting, take the rest. As in the tile kernel a CTA does a split of the rows' steps where CTAs are few.
 #include <atomic>
 
 #include "exact_tile.cuh"

@@ -26,7 +26,6 @@ struct TileArgs {
     float *pre_ml, *pre_o;             // ... or records [B H][nsp][m G][2] and [..][128]
                                        // (prefix: [H][nsp][sequences G])
     float scale_log2;
-    int sms;
 };
 
 // Maps of q (channels, q-heads, tokens, sequences) in boxes of 64 channels; of the rows (64 channels,

@@ -124,6 +124,17 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(0), "r"(head), "r"(seq), "r"(bar)
         : "memory");
 }
+// The same for rows that leave L2 before other data does: decode with accumulated weights reads rows
+// once and its scores twice (8 x 32768 rows: 187 -> 183 us, ragged float32 29.6 -> 27.8 us).
+__device__ __forceinline__ void tma_load_5d_once(uint32_t dst, const CUtensorMap *map, int row,
+                                                 int head, int seq, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .b64 p;\n\tcreatepolicy.fractional.L2::evict_first.b64 p, 1.0;\n\t"
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], p;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(0), "r"(head), "r"(seq), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
     for (uint32_t i = 0; i < EX_POLLS; ++i) {
         uint32_t done;
