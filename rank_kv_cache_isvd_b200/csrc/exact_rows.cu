@@ -7,7 +7,8 @@
 // of key and value units in shared memory. (The split kernel, which gives each tile of 8 rows its own
 // copy of the rows, was bound by L2 here: 950 us against 425 us at 94 x 4 queries of 8 kv-heads over
 // 7264 shared rows.) The same products reach 73 TFLOP/s (130 x 8 queries over 16384 shared rows:
-// 957 us); fetching and decoding instructions, then the splitting, take the rest. As in the tile kernel a CTA does a split of the rows' steps where CTAs are few.
+// 957 us); fetching and decoding instructions, then the splitting, take the rest. As in the tile
+// kernel a CTA does a split of the rows' steps where CTAs are few.
 #include <atomic>
 
 #include "exact_tile.cuh"
