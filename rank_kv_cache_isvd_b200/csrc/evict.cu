@@ -105,11 +105,9 @@ __global__ void __launch_bounds__(SEL_T, 1) evict_select_kernel(EvictArgs a, int
     int *src = a.moves + (long long)unit * 2 * a.max_moves, *dst = src + a.max_moves;
     const int R = min(n, a.budget);
     if (FUSED) {
-        // all blocks of the sequence have read its length, which lens_out may replace
-        if (a.H > 1) {
-            __syncthreads();
-            cluster_sync();
-        }
+        // all threads of the sequence's blocks have read its length, which lens_out may replace
+        __syncthreads();
+        if (a.H > 1) cluster_sync();
         if (tid == 0 && h == 0) a.lens_out[b] = R;
     } else if (tid == 0 && rank == 0) {
         a.keep[unit] = R;

@@ -287,6 +287,22 @@ def test_evict(B, H, n, budget, recent, sinks, rt, lens, in_place, ties):
             assert torch.equal(po[b, h].cpu()[keep:], rest_p[keep:])
 
 
+def test_evict_of_single_heads_replaces_lengths_in_place():
+    """One launch, one block per sequence: no warp may read a length that another has replaced."""
+    B, n, budget = 200, 900, 600
+    k, v, mass, pos = _evict_inputs(_gen(16), B, 1, n, "bf16", False)
+    m0, p0 = mass.cpu().numpy().copy(), pos.cpu().numpy().copy()
+    nl = [n - 2 * b for b in range(B)]
+    want = [evicted(m0[b, 0], p0[b, 0], nl[b], budget, 32, 4) for b in range(B)]
+    for _ in range(20):
+        m, p, ls = torch.from_numpy(m0).cuda(), torch.from_numpy(p0).cuda(), _i32(nl)
+        _cache(k, v, ls).evict(m, p, budget=budget, recent=32, sinks=4)
+        assert ls.tolist() == [min(x, budget) for x in nl]
+        for b, (slots, keep) in enumerate(want):
+            assert np.array_equal(m[b, 0].cpu().numpy()[:keep], m0[b, 0][slots])
+            assert np.array_equal(p[b, 0].cpu().numpy()[:keep], p0[b, 0][slots])
+
+
 def test_evict_weights_that_are_not_finite():
     """NaN and infinite weights order above finite ones and never lose a fixed row."""
     k, v, mass, pos = _evict_inputs(_gen(7), 1, 1, 200, "bf16", False)
