@@ -467,10 +467,13 @@ extern "C" int iskv_prefix_decode_workspace(const iskv_exact_rows *r, const iskv
         !stride_ok(p->head_stride, r->n_kv_heads, e) || !stride_ok(p->row_stride, p->rows, e) ||
         (p->rows > 1 && p->row_stride < EX_D))
         return ISKV_ERR_INVALID_ARG;
-    const int sms = sm_count();
-    if (!sms) return ISKV_ERR_CUDA;
     const int tpt = ex_tpt(q->n_q_heads / r->n_kv_heads);
     const long long tiles = (r->batch + tpt - 1) / tpt;
+    // one tile: the split kernel takes the prefix, and counts its steps in 32 bits with the others
+    if (tiles == 1 && (long long)r->n_kv_heads * (p->rows / 16 + 3) > 0x7fffffffLL)
+        return ISKV_ERR_UNSUPPORTED;
+    const int sms = sm_count();
+    if (!sms) return ISKV_ERR_CUDA;
     size_t records = 0;
     for (int tile = 0; tile <= (all_bf16(r, q) ? 1 : 0); ++tile) {
         const size_t b = tile_record_bytes(prefix_plan(r, q, p, tile != 0, sms), r->n_kv_heads,

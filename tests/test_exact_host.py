@@ -99,6 +99,16 @@ def test_bad_prefixes_are_refused(bad):
     assert iskv.iskv_prefix_decode(_rows(), _queries(), None, *WS, stream=0) == INVALID
 
 
+def test_prefixes_of_more_steps_than_32_bits_are_refused():
+    """A prefix that the split kernel takes by itself, one tile of query rows for each of many
+    kv-heads that share it."""
+    r = _rows(batch=1, n_kv_heads=4096, rows=1)
+    q = _queries(n_q_heads=4096)
+    p = _prefix(head_stride=0, rows=1 << 24)
+    assert iskv.iskv_prefix_decode_workspace(r, q, p)[0] == UNSUPPORTED
+    assert iskv.iskv_prefix_decode(r, q, p, *WS, stream=0) == UNSUPPORTED
+
+
 def test_eviction_refuses_what_it_cannot_keep_or_move():
     ok = (256, 256, 256, 256, 256)
     r = _rows()
