@@ -34,8 +34,8 @@ class ExactKVCache:
     ``None``: all. The tensors are read at each call: rows written and lengths advanced between
     calls count.
 
-    Calls run on the current stream of the tensors' device, or on ``stream``, and synchronise
-    nothing. They share the object's workspace: calls that may overlap (other streams, graphs
+    Calls run on the current stream of the tensors' device, or as if ``stream`` were that one, and
+    synchronise nothing. They share the object's workspace: calls that may overlap (other streams, graphs
     replayed at the same time) need objects of their own, which may hold the same tensors. A
     captured call uses addresses of this object's workspace, so the object has to outlive the
     graph. An object is not thread-safe.
@@ -63,6 +63,7 @@ class ExactKVCache:
         self._rows_at = ctypes.addressof(self._rows)
         self._plans: dict = {}          # per form of a call: its structs and workspace size
         self._ws: torch.Tensor | None = None
+        self._ws_stream = 0             # whose memory it is
         self._old_ws: list = []         # captured graphs may hold their addresses
 
     # -- plumbing --------------------------------------------------------------------------------
@@ -72,16 +73,22 @@ class ExactKVCache:
             raise ValueError(f"{what} must be contiguous, {dtype} of shape {tuple(shape)} on "
                              f"{self.device}")
 
-    def _stream(self, stream, *owned) -> int:
-        if stream is None:
-            return torch._C._cuda_getCurrentRawStream(self._index)
+    def _under(self, stream):
+        """Makes ``stream`` (a torch stream of the device, or a raw handle) the current one: what a
+        call allocates then comes from that stream's memory."""
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=self.device)
-        if stream != torch.cuda.current_stream(self.device):
-            # what this call allocated must not be reused before `stream` is done with it
-            for x in owned:
-                x.record_stream(stream)
-        return stream.cuda_stream
+            stream = (torch.cuda.ExternalStream(stream, device=self.device) if stream else
+                      torch.cuda.default_stream(self.device))
+        elif stream.device != self.device:
+            raise ValueError(f"stream must be of {self.device}")
+        return torch.cuda.stream(stream)
+
+    def _stream(self) -> int:
+        """The current stream; the workspace is not handed out before its work on it is done."""
+        raw = torch._C._cuda_getCurrentRawStream(self._index)
+        if raw != self._ws_stream:
+            self._ws.record_stream(torch.cuda.current_stream(self.device))
+        return raw
 
     def _plan(self, key, make):
         """The plan of a call's form; ``make(plan)`` fills a new one and asks for its workspace."""
@@ -98,6 +105,7 @@ class ExactKVCache:
             if self._ws is not None:
                 self._old_ws.append(self._ws)
             self._ws = torch.empty((plan.need,), dtype=torch.uint8, device=self.device)
+            self._ws_stream = torch._C._cuda_getCurrentRawStream(self._index)
         return plan
 
     def _queries(self, plan, q: torch.Tensor, out: torch.Tensor, tokens: bool):
@@ -139,8 +147,10 @@ class ExactKVCache:
         ``[batch][n_q][m][128]``: token i sits at position ``p = lens[b] - q_lens[b] + i`` and sees
         the rows ``j <= p`` with ``j < sinks`` or ``j > p - window``. A token that sees nothing gets
         zeros; outputs of tokens ``i >= q_lens[b]`` are not written."""
-        made = out is None
-        if made:
+        if stream is not None:
+            with self._under(stream):
+                return self.window_attn(q, window=window, sinks=sinks, q_lens=q_lens, out=out)
+        if out is None:
             out = torch.empty_like(q)
 
         def make(plan):
@@ -155,7 +165,7 @@ class ExactKVCache:
         if q_lens is not None:
             self._check(q_lens, "q_lens", torch.int32, self._batch_shape)
             x.q_lens = q_lens.data_ptr()
-        s = self._stream(stream, ws, out) if made else self._stream(stream, ws)
+        s = self._stream()
         self._call("iskv_window_attn", lib.iskv_window_attn, self._rows_at, plan.x_at, window, sinks,
                    ws.data_ptr(), plan.need, s)
         return out
@@ -167,13 +177,15 @@ class ExactKVCache:
         rows. Adds each row's attention weight, summed over the q-heads of its kv-head, to ``mass``
         (float32 ``[batch][n_kv][rows]``), in place or into ``mass_out``. Returns
         ``(out, mass_out)``."""
+        if stream is not None:
+            with self._under(stream):
+                return self.mass_decode(q, mass, mass_out=mass_out, out=out)
         self._check(mass, "mass", torch.float32, self._mass_shape)
         if mass_out is None:
             mass_out = mass
         else:
             self._check(mass_out, "mass_out", torch.float32, self._mass_shape)
-        made = out is None
-        if made:
+        if out is None:
             out = torch.empty_like(q)
 
         def make(plan):
@@ -185,7 +197,7 @@ class ExactKVCache:
         self._on_device(q, out)
         x, ws = plan.x, self._ws
         x.q, x.out = q.data_ptr(), out.data_ptr()
-        s = self._stream(stream, ws, out) if made else self._stream(stream, ws)
+        s = self._stream()
         self._call("iskv_mass_decode", lib.iskv_mass_decode, self._rows_at, plan.x_at,
                    mass.data_ptr(), mass_out.data_ptr(), ws.data_ptr(), plan.need, s)
         return out, mass_out
@@ -199,6 +211,10 @@ class ExactKVCache:
         the lowest slot). Rows move in place; ``mass`` (float32), ``pos`` (int32, both
         ``[batch][n_kv][rows]``) and the lengths are updated in place or into the ``*_out``
         tensors. Without ``lens_out`` the cache needs its own ``lens``."""
+        if stream is not None:
+            with self._under(stream):
+                return self.evict(mass, pos, budget=budget, recent=recent, sinks=sinks,
+                                  mass_out=mass_out, pos_out=pos_out, lens_out=lens_out)
         mass_out = mass if mass_out is None else mass_out
         pos_out = pos if pos_out is None else pos_out
         lens_out = self.lens if lens_out is None else lens_out
@@ -216,14 +232,16 @@ class ExactKVCache:
         ws = self._ws
         self._call("iskv_evict", lib.iskv_evict, self._rows_at, mass.data_ptr(), mass_out.data_ptr(),
                    pos.data_ptr(), pos_out.data_ptr(), lens_out.data_ptr(), budget, recent, sinks,
-                   ws.data_ptr(), plan.need, self._stream(stream, ws))
+                   ws.data_ptr(), plan.need, self._stream())
 
     def prefix_decode(self, q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Tensor, *,
                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Decode attention of one token per sequence (``q`` ``[batch][n_q][128]``) over the rows
         ``prefix_k``, ``prefix_v`` (``[n_kv][P][128]``) that all sequences share, and its own."""
-        made = out is None
-        if made:
+        if stream is not None:
+            with self._under(stream):
+                return self.prefix_decode(q, prefix_k, prefix_v, out=out)
+        if out is None:
             out = torch.empty_like(q)
 
         def make(plan):
@@ -247,7 +265,7 @@ class ExactKVCache:
         x, p, ws = plan.x, plan.p, self._ws
         x.q, x.out = q.data_ptr(), out.data_ptr()
         p.k, p.v = prefix_k.data_ptr(), prefix_v.data_ptr()
-        s = self._stream(stream, ws, out) if made else self._stream(stream, ws)
+        s = self._stream()
         self._call("iskv_prefix_decode", lib.iskv_prefix_decode, self._rows_at, plan.x_at, plan.p_at,
                    ws.data_ptr(), plan.need, s)
         return out

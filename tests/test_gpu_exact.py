@@ -378,6 +378,67 @@ def test_calls_on_another_stream_and_in_graphs():
         assert torch.equal(o, want) and torch.equal(mo, want_m)
 
 
+def _workspace_of(cache):
+    return cache._ws.data_ptr(), cache._ws.numel()
+
+
+@pytest.mark.parametrize("by_argument", [False, True])
+def test_a_workspace_in_use_on_another_stream_is_not_handed_out(by_argument):
+    """An object that goes while its last call is still due on another stream: the memory of its
+    workspace must not come back from the allocator before that call has run."""
+    g = _gen(17)
+    k, v = _kv(g, 2, 2, 600, "bf16")
+    q = torch.randn((2, 4, D), generator=g, device="cuda")
+    mass = torch.zeros((2, 2, 600), device="cuda")
+    want = _cache(k, v).mass_decode(q, mass, mass_out=torch.zeros_like(mass))[1]
+    out, got = torch.zeros_like(q), torch.zeros_like(mass)
+    cache = _cache(k, v)
+    cache.mass_decode(q, mass, mass_out=torch.zeros_like(mass), out=out)     # sized on this stream
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)                                       # some 50 ms
+    if by_argument:
+        cache.mass_decode(q, mass, mass_out=got, out=out, stream=side)
+    else:
+        with torch.cuda.stream(side):
+            cache.mass_decode(q, mass, mass_out=got, out=out)
+    at, size = _workspace_of(cache)
+    del cache
+    again = torch.empty((size,), dtype=torch.uint8, device="cuda")
+    assert not side.query()                              # the call has not run yet
+    assert again.data_ptr() != at
+    again.fill_(255)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_what_a_call_allocates_belongs_to_its_stream():
+    """With `stream`, outputs and workspace come from that stream's memory, not from what the
+    current one may still be using."""
+    g = _gen(18)
+    k, v = _kv(g, 1, 2, 300, "bf16")
+    q = torch.randn((1, 4, 1, D), generator=g, device="cuda")
+    want = _cache(k, v).window_attn(q, window=300)
+    torch.cuda.synchronize()
+    need = 4 * (1 << 20)
+    busy = torch.empty((need,), dtype=torch.uint8, device="cuda")
+    out_busy = torch.empty_like(q)
+    torch.cuda._sleep(100_000_000)
+    held = {busy.data_ptr(): need, out_busy.data_ptr(): out_busy.numel() * 4}
+    del busy, out_busy                                   # free to this stream, behind its sleep
+    side, cache = torch.cuda.Stream(), _cache(k, v)
+    out = cache.window_attn(q, window=300, stream=side)
+    assert not torch.cuda.current_stream().query()       # this stream is not through
+    at, size = _workspace_of(cache)
+    for lo, n in held.items():
+        assert not (lo <= at < lo + n or at <= lo < at + size)
+        assert out.data_ptr() != lo
+    side.synchronize()
+    assert torch.equal(out, want)
+    torch.cuda.synchronize()
+
+
 def test_every_call_captured_without_a_first_one():
     """All calls in one graph of a fresh object (its workspace and plans are made while capturing),
     replayed on new contents: the same bits as eager calls."""
