@@ -356,7 +356,7 @@ typedef struct {
 
 typedef struct {
     const void *q;           /* element (b, g, i, c) at b seq + g head + i tok + c; 16-byte aligned */
-    void *out;               /* the same with the o_ strides                                      */
+    void *out;               /* the same with the o_ strides; must not overlap anything that is read */
     long long q_seq_stride, q_head_stride, q_tok_stride;
     long long o_seq_stride, o_head_stride, o_tok_stride;
     int n_q_heads;           /* n_kv_heads times 1 .. 8                                           */

@@ -125,6 +125,15 @@ class ExactKVCache:
                                     q.shape[2] if tokens else 1, _TYPES[q.dtype], None)
         plan.x_at = ctypes.addressof(plan.x)
 
+    @staticmethod
+    def _apart(q: torch.Tensor, out: torch.Tensor):
+        """Addresses of queries and outputs. Blocks that share queries read them at different times,
+        so outputs cannot take their place."""
+        at, to = q.data_ptr(), out.data_ptr()
+        if at == to and q.numel():
+            raise ValueError("out must not be q")
+        return at, to
+
     def _on_device(self, *tensors) -> None:
         for x in tensors:
             if x.get_device() != self._index:
@@ -161,7 +170,8 @@ class ExactKVCache:
                            out.dtype, window, sinks), make)
         self._on_device(q, out)
         x, ws = plan.x, self._ws
-        x.q, x.out, x.q_lens = q.data_ptr(), out.data_ptr(), None
+        x.q, x.out = self._apart(q, out)
+        x.q_lens = None
         if q_lens is not None:
             self._check(q_lens, "q_lens", torch.int32, self._batch_shape)
             x.q_lens = q_lens.data_ptr()
@@ -196,7 +206,7 @@ class ExactKVCache:
                            out.dtype), make)
         self._on_device(q, out)
         x, ws = plan.x, self._ws
-        x.q, x.out = q.data_ptr(), out.data_ptr()
+        x.q, x.out = self._apart(q, out)
         s = self._stream()
         self._call("iskv_mass_decode", lib.iskv_mass_decode, self._rows_at, plan.x_at,
                    mass.data_ptr(), mass_out.data_ptr(), ws.data_ptr(), plan.need, s)
@@ -263,7 +273,7 @@ class ExactKVCache:
                            prefix_v.stride(), prefix_k.dtype, prefix_v.dtype), make)
         self._on_device(q, out, prefix_k, prefix_v)
         x, p, ws = plan.x, plan.p, self._ws
-        x.q, x.out = q.data_ptr(), out.data_ptr()
+        x.q, x.out = self._apart(q, out)
         p.k, p.v = prefix_k.data_ptr(), prefix_v.data_ptr()
         s = self._stream()
         self._call("iskv_prefix_decode", lib.iskv_prefix_decode, self._rows_at, plan.x_at, plan.p_at,

@@ -568,3 +568,16 @@ def test_small_workspaces_and_wrong_tensors_are_refused():
     code, need = iskv.iskv_window_attn_workspace(c._rows, form, 8, 0)
     assert code == 0
     assert iskv.iskv_window_attn(c._rows, form, 8, 0, c._ws, need - 1) == iskv.ISKV_ERR_CAPACITY
+
+
+def test_outputs_in_place_of_queries_are_refused():
+    k, v = _kv(_gen(19), 1, 1, 64, "bf16")
+    q, pk, pv = torch.zeros((1, 1, 1, D), device="cuda"), k[0].clone(), v[0].clone()
+    mass = torch.zeros((1, 1, 64), device="cuda")
+    cache = _cache(k, v)
+    with pytest.raises(ValueError):
+        cache.window_attn(q, window=8, out=q)
+    with pytest.raises(ValueError):
+        cache.mass_decode(q[:, :, 0], mass, out=q[:, :, 0])
+    with pytest.raises(ValueError):
+        cache.prefix_decode(q[:, :, 0], pk, pv, out=q[:, :, 0])
