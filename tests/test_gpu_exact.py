@@ -581,3 +581,85 @@ def test_outputs_in_place_of_queries_are_refused():
         cache.mass_decode(q[:, :, 0], mass, out=q[:, :, 0])
     with pytest.raises(ValueError):
         cache.prefix_decode(q[:, :, 0], pk, pv, out=q[:, :, 0])
+
+
+def _whole(q, k, v):
+    """64-bit attention of q [r][128] over all of k, v [n][128], on the device in chunks: weights
+    [r][n], outputs, and what ``out_bound`` asks of an ``Attended``."""
+    ref, chunk = Attended.__new__(Attended), 1 << 20
+    q = q.double()
+    s = torch.empty((q.shape[0], k.shape[0]), dtype=torch.float64, device=k.device)
+    ref.terms = torch.zeros((q.shape[0], 1), dtype=torch.float64, device=k.device)
+    for i in range(0, k.shape[0], chunk):
+        x = k[i:i + chunk].double()
+        s[:, i:i + chunk] = (q @ x.T) * D ** -0.5
+        size = (q.abs() @ x.abs().T) * D ** -0.5
+        ref.terms = torch.maximum(ref.terms, size.amax(-1, keepdim=True))
+    ref.w = torch.softmax(s, -1)
+    ref.o, ref.spread = (torch.zeros_like(q) for _ in range(2))
+    for i in range(0, k.shape[0], chunk):
+        x = v[i:i + chunk].double()
+        ref.o += ref.w[:, i:i + chunk] @ x
+        ref.spread += ref.w[:, i:i + chunk] @ x.abs()
+    ref.n = k.shape[0]
+    return ref
+
+
+def test_offsets_past_32_bits():
+    """Rows of one cache past 2^31 elements (2^32 bytes), by every call: the last rows count."""
+    g = _gen(20)
+    H, G, n = 2, 2, (1 << 23) + 5
+    k, v = (torch.randn((1, n, H, D), generator=g, device="cuda", dtype=torch.bfloat16).transpose(1, 2)
+            for _ in range(2))
+    assert (n - 1) * k.stride(2) + D > 1 << 31
+    cache = _cache(k, v, _i32([n]))
+    # window: single token (split kernel) and a chunk (tile kernel); near rows and three sinks
+    for m in (1, 70):
+        q = torch.randn((1, H * G, m, D), generator=g, device="cuda").bfloat16()
+        out = cache.window_attn(q, window=200, sinks=3)
+        near = 300
+        pick = torch.cat([torch.arange(3), torch.arange(n - near, n)]).cuda()
+        j, p = pick.cpu().numpy()[None], (n - m + np.arange(m))[:, None]
+        see = (j <= p) & ((j < 3) | (j > p - 200))
+        for x in range(H * G):
+            ref = Attended(q[0, x], k[0, x // G][pick], v[0, x // G][pick], see)
+            err = (out[0, x].double().cpu() - ref.o).abs()
+            assert (err <= out_bound(ref, q.dtype, torch.bfloat16)).all()
+    # accumulated weights over all rows, the last of them made to stand out
+    q = torch.randn((1, H * G, D), generator=g, device="cuda")
+    k[0, :, n - 1] = 4 * q[0, ::G].bfloat16()
+    mass = torch.zeros((1, H, n), device="cuda")
+    out, mass = cache.mass_decode(q, mass)
+    for h in range(H):
+        ref = _whole(q[0, h * G:(h + 1) * G], k[0, h], v[0, h])
+        err = (out[0, h * G:(h + 1) * G].double() - ref.o).abs()
+        assert (err <= out_bound(ref, q.dtype)).all()
+        err = (mass[0, h].double() - ref.w.sum(0)).abs()
+        assert (err <= (ref.w * weight_bound(ref)).sum(0) + ref.w.sum(0) * G * 2.0 ** -24 + 1e-30).all()
+        assert mass[0, h, n - 1] > 0.01
+        del ref, err
+    # the rows as a prefix of three sequences
+    q = torch.randn((3, H * G, D), generator=g, device="cuda").bfloat16()
+    own_k, own_v = _kv(g, 3, H, 4, "bf16")
+    out = _cache(own_k, own_v, _i32([0, 0, 0])).prefix_decode(q, k[0], v[0])
+    for h in range(H):
+        ref = _whole(q[:, h * G:(h + 1) * G].reshape(3 * G, D), k[0, h], v[0, h])
+        err = (out[:, h * G:(h + 1) * G].reshape(3 * G, D).double() - ref.o).abs()
+        assert (err <= out_bound(ref, q.dtype, torch.bfloat16)).all()
+        del ref, err
+    # eviction: rows from the far end move down
+    budget = n - 3000
+    mass = torch.rand((1, H, n), generator=g, device="cuda")
+    pos = torch.arange(n, device="cuda", dtype=torch.int32).expand(1, H, n).contiguous()
+    k0, v0, m0, p0 = k[0].clone(), v[0].clone(), mass.cpu().numpy(), pos.cpu().numpy()
+    cache.evict(mass, pos, budget=budget, recent=100, sinks=4)
+    assert cache.lens.tolist() == [budget]
+    for h in range(H):
+        slots, keep = evicted(m0[0, h], p0[0, h], n, budget, 100, 4)
+        at = torch.from_numpy(slots).cuda()
+        assert int((at != torch.arange(keep, device="cuda")).sum()) > 1000
+        assert torch.equal(pos[0, h, :keep].long(), at)
+        for i in range(0, keep, 1 << 20):
+            part = slice(i, min(keep, i + (1 << 20)))
+            assert torch.equal(k[0, h, part], k0[h][at[part]])
+            assert torch.equal(v[0, h, part], v0[h][at[part]])
