@@ -60,7 +60,8 @@ __device__ __forceinline__ uint32_t evict_key(float w, int pos, int sinks, int l
 template <int E, bool FUSED>
 __global__ void __launch_bounds__(SEL_T, 1) evict_select_kernel(EvictArgs a, int cluster) {
     __shared__ unsigned hist[2][BINS];
-    __shared__ unsigned sh[SEL_W], sh2[SEL_W];
+    __shared__ unsigned sh[SEL_W];
+    __shared__ uint4 of_warp[SEL_W];
     __shared__ unsigned found[2];                    // digit, keys above it
     __shared__ unsigned counts[4];                   // of this block: > T, = T, the same below R
     __shared__ int sh_latest;
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(SEL_T, 1) evict_select_kernel(EvictArgs a, int
                 const int j0 = turn + (warp * E + e) * 32;
                 if (j0 >= hi) break;
                 const bool in = j0 + lane < hi && (key[e] & mask) == T;
+                if (!__any_sync(0xffffffffu, in)) continue;      // most, from the second digit on
                 const unsigned d = (key[e] >> shift) & ((1u << bits) - 1u);
                 // one digit in the whole warp (many equal weights): one atomic
                 const unsigned d0 = __shfl_sync(0xffffffffu, d, 0);
@@ -227,39 +229,51 @@ __global__ void __launch_bounds__(SEL_T, 1) evict_select_kernel(EvictArgs a, int
         // this buffer is used again by the third digit, which all blocks begin after the second's
         // cluster barrier: no block then reads the first's counts
         __syncthreads();
-        if (digit == 1)
-            for (int i = tid; i < BINS; i += SEL_T) hist[0][i] = 0;
         T |= found[0] << shift;
         above = found[1];
         mask |= ((1u << bits) - 1u) << shift;
-        __syncthreads();
+        if (digit == 1) {
+            for (int i = tid; i < BINS; i += SEL_T) hist[0][i] = 0;
+            __syncthreads();
+        }
     }
     const int ties = R - (int)above;                 // keys equal to T that stay: the lowest slots
 
-    // counts of this block, then of the blocks before it and of all
-    if (tid < 4) counts[tid] = 0;
-    __syncthreads();
+    // keys > T, = T, the same below R: of each warp, of the block, of the blocks before it and of all
+    unsigned c[4] = {0, 0, 0, 0};
     for (int turn = lo; turn < hi; turn += TURN) {
         if (!one) fetch(turn);
-        int c[4] = {0, 0, 0, 0};
+        unsigned all = 0, under = 0;                 // two counts each, of at most 32 E
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const int j = turn + (warp * E + e) * 32 + lane;
-            const bool gt = j < hi && key[e] > T, eq = j < hi && key[e] == T;
-            c[0] += gt;
-            c[1] += eq;
-            c[2] += gt && j < R;
-            c[3] += eq && j < R;
+            const unsigned x = j >= hi ? 0u : key[e] > T ? 1u : key[e] == T ? 1u << 16 : 0u;
+            all += x;
+            under += j < R ? x : 0u;
         }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            c[x] = __reduce_add_sync(0xffffffffu, c[x]);
-            if (lane == 0 && c[x]) atomicAdd(&counts[x], (unsigned)c[x]);
-        }
+        all = __reduce_add_sync(0xffffffffu, all);
+        under = __reduce_add_sync(0xffffffffu, under);
+        c[0] += all & 0xffffu;
+        c[1] += all >> 16;
+        c[2] += under & 0xffffu;
+        c[3] += under >> 16;
     }
+    if (lane == 0) of_warp[warp] = make_uint4(c[0], c[1], c[2], c[3]);
     __syncthreads();
-    int gt_before = 0, eq_before = 0, low_gt = (int)counts[2], low_eq = (int)counts[3];
+    const uint4 cw = of_warp[lane];
+    int gt_before = 0, eq_before = 0;
+    int low_gt = (int)__reduce_add_sync(0xffffffffu, cw.z);
+    int low_eq = (int)__reduce_add_sync(0xffffffffu, cw.w);
     if (cluster > 1) {
+        const unsigned gt_here = __reduce_add_sync(0xffffffffu, cw.x);
+        const unsigned eq_here = __reduce_add_sync(0xffffffffu, cw.y);
+        if (tid == 0) {
+            counts[0] = gt_here;
+            counts[1] = eq_here;
+            counts[2] = (unsigned)low_gt;
+            counts[3] = (unsigned)low_eq;
+        }
+        __syncwarp();
         cluster_sync();
         low_gt = low_eq = 0;
         for (int x = 0; x < cluster; ++x) {
@@ -270,31 +284,34 @@ __global__ void __launch_bounds__(SEL_T, 1) evict_select_kernel(EvictArgs a, int
             low_gt += (int)of_rank(&counts[2], x);
             low_eq += (int)of_rank(&counts[3], x);
         }
-        cluster_sync();                              // no block ends while others read its counts
+        // no block ends while others read its counts: the wait is at the end
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     }
     const int low = low_gt + min(low_eq, ties);      // kept rows of slots < R
     const unsigned below = (1u << lane) - 1u;
     for (int turn = lo; turn < hi; turn += TURN) {
         if (!one) fetch(turn);
-        int gt = 0, eq = 0;
+        uint4 x = cw;                                // the warps' counts of this turn
+        if (!one) {
+            unsigned all = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int j = turn + (warp * E + e) * 32 + lane;
-            gt += j < hi && key[e] > T;
-            eq += j < hi && key[e] == T;
+            for (int e = 0; e < E; ++e) {
+                const int j = turn + (warp * E + e) * 32 + lane;
+                all += j >= hi ? 0u : key[e] > T ? 1u : key[e] == T ? 1u << 16 : 0u;
+            }
+            all = __reduce_add_sync(0xffffffffu, all);
+            __syncthreads();
+            if (lane == 0) sh[warp] = all;
+            __syncthreads();
+            x.x = sh[lane] & 0xffffu;
+            x.y = sh[lane] >> 16;
         }
-        gt = __reduce_add_sync(0xffffffffu, gt);
-        eq = __reduce_add_sync(0xffffffffu, eq);
-        __syncthreads();
-        if (lane == 0) {
-            sh[warp] = (unsigned)gt;
-            sh2[warp] = (unsigned)eq;
+        int g0 = gt_before + (int)__reduce_add_sync(0xffffffffu, lane < warp ? x.x : 0u);
+        int e0 = eq_before + (int)__reduce_add_sync(0xffffffffu, lane < warp ? x.y : 0u);
+        if (!one) {
+            gt_before += (int)__reduce_add_sync(0xffffffffu, x.x);
+            eq_before += (int)__reduce_add_sync(0xffffffffu, x.y);
         }
-        __syncthreads();
-        int g0 = gt_before + (int)__reduce_add_sync(0xffffffffu, lane < warp ? sh[lane] : 0u);
-        int e0 = eq_before + (int)__reduce_add_sync(0xffffffffu, lane < warp ? sh2[lane] : 0u);
-        gt_before += (int)__reduce_add_sync(0xffffffffu, sh[lane]);
-        eq_before += (int)__reduce_add_sync(0xffffffffu, sh2[lane]);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const int j0 = turn + (warp * E + e) * 32, j = j0 + lane;
@@ -317,6 +334,10 @@ __global__ void __launch_bounds__(SEL_T, 1) evict_select_kernel(EvictArgs a, int
     }
     if (!FUSED) {
         if (tid == 0 && rank == 0) a.n_moves[unit] = R - low;
+        if (cluster > 1) {
+            __syncwarp();
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        }
         return;
     }
     __syncthreads();                                 // the lists are complete
