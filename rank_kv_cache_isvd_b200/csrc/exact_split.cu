@@ -329,8 +329,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                                  : "memory");
                     const int hd = it.h * (it.b < 0 ? a.p_head_mul : a.head_mul);
                     const int sq = it.b < 0 ? 0 : it.b * a.seq_mul;
-                    if (MASS) tma_load_5d_once(ring + ld_at * UNIT, map, row, hd, sq, b);
-                    else tma_load_5d(ring + ld_at * UNIT, map, row, hd, sq, b);
+                    tma_load_5d_once(ring + ld_at * UNIT, map, row, hd, sq, b);
                 }
                 ns += loads & 1;
                 ++loads;
