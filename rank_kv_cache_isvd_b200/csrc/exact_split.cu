@@ -3,17 +3,17 @@
 //   o_q = sum_j p_qj v_j / sum_j p_qj,   p_qj = 2^(s_qj - m_q),   s_qj = q . k_j log2(e)/sqrt(128)
 //
 // Decode reads every visible key and value once and does 4 G flops per pair of their bytes: it is
-// bound by HBM. So the layout serves the loads. A warp owns 16 rows of a step at a time and a ring
-// of three such stages in shared memory, which it fills by TMA (one box of keys, one of values) and
-// waits for by itself: no barrier joins the warps until the end of an item, and 128 KB per SM are in
-// flight. (Loads by cp.async, one per 16 bytes, cost 750 instructions per warp and step, two thirds
-// of them for addresses: 220 us at 8 x 32768 rows of 8 kv-heads.)
+// bound by HBM. So the layout serves the loads. A warp owns 32 bf16 (16 float32) rows of a step and a
+// ring of three units of 8 KB in shared memory, which it fills by TMA (keys and values in turn) and
+// waits for by itself: no barrier joins the warps until the end of an item, and up to 192 KB per SM are
+// in flight (6.8 TB/s while they stream). (Loads by cp.async, one per 16 bytes, cost 750 instructions
+// per warp and step, two thirds of them for addresses: 220 us at 8 x 32768 rows of 8 kv-heads.)
 //
 // The products of a warp's 8 query rows are in exact_warp.cuh.
 //
 // Behind a kernel that does a shared prefix (it starts on the SMs that the other leaves) the records of
 // that one join where an item ends. (Two kernels side by side on parts of the SMs, with all records
-// joined by the merge kernel, took 77 to 94 us instead of 73 at 130 sequences, the merge 12 of them.)
+// joined by the merge kernel, took 77 to 94 us at 130 sequences where this took 73, the merge 12 of them.)
 //
 // Teams of 1, 2, 4 or 8 warps work by themselves. By items: a team takes whole items; long ones go to
 // a block or a cluster of up to 8 blocks that share out the item's steps and join their results

@@ -25,7 +25,7 @@
 // exactly enough: P is at most 256). Moving it rescales O in tensor memory, which the softmax warp
 // does itself: S of this block being complete says that the P V before it is too.
 //
-// P is rounded to bf16 (half a step, 2^-9 of the leading bits' scale, at random over the keys);
+// P is rounded to bf16 (half a step, up to 2^-8 of a weight, at random over the keys);
 // the sum l takes the unrounded values, and all sums are float32.
 //
 // Every wait is bounded. A wait that gives up sets the CTA's abort flag and the device's status

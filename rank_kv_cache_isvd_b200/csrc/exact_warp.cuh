@@ -6,7 +6,7 @@
 // - bf16 rows (m16n8k16, bf16): float32 queries are split in three bf16 terms (24 bits), x = hi + mid
 //   + lo: hi sits in rows 0-7 of the A operand and mid in rows 8-15, so one instruction does both terms
 //   and both sums land in one thread; lo takes a second one. The weights p likewise, so that float32
-//   outputs keep float32 accuracy (a weight rounded to bf16 would cost 2^-9); for bf16 outputs their
+//   outputs keep float32 accuracy (a weight rounded to bf16 would cost up to 2^-8); for bf16 outputs their
 //   first two terms are used, which cost no more than one.
 // - float32 rows (m16n8k8, tf32): every operand is split in two tf32 terms (22 bits), the queries' and
 //   weights' in rows 0-7 and 8-15: (hi | lo) x hi and (hi | 0) x lo. Three bf16 terms took half as many
