@@ -81,6 +81,10 @@ WINDOW_CASES = [
     (1, 1, 4, 5000, 9, 4000, 100, "bf16", "bf16", None, None, False),
     (70, 8, 2, 700, 1, 300, 40, "bf16", "bf16", list(range(1, 701, 10)), None, False),
     (160, 2, 4, 90, 2, 1000, 0, "f32", "bf16", [90] * 160, [2, 0] * 80, True),
+    # more pairs of tiles than SMs, the last round nearly empty; odd and missing tokens
+    (3, 8, 4, 420, 420, 100, 3, "bf16", "bf16", None, None, True),
+    (4, 13, 8, 96, 90, 1000, 0, "bf16", "bf16", [96, 80, 5, 0], [90, 31, 9, 0], False),
+    (13, 12, 1, 200, 130, 70, 5, "bf16", "bf16", list(range(188, 201)), list(range(0, 130, 10)), True),
 ]
 
 
