@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "exact_order.cuh"
 #include "iskv.h"
 
 namespace iskv {
@@ -77,14 +78,6 @@ struct ExactSpan {
     int RT;           // tiles per kv-head
 };
 
-// Length of the order in which a tile of tpt tokens visits the rows, at most: its window, and the
-// sinks in groups of 32. Sinks that the window does not reach fill up their last group.
-__host__ __device__ inline int ex_most_rows(int window, int sinks, int tpt, int n) {
-    const long long most = (long long)((sinks + 31) & ~31) + window + tpt - 1;
-    const int all = window >= n ? n : n + 31;
-    return most < all ? (int)most : all;
-}
-
 __device__ __forceinline__ ExactSpan ex_shared_span(const ExactArgs &a, int rs) {
     ExactSpan s;
     const int tpt = ex_tpt(a.G);
@@ -94,26 +87,26 @@ __device__ __forceinline__ ExactSpan ex_shared_span(const ExactArgs &a, int rs) 
 }
 // Sequence of n rows and ql tokens. An item has a step even where nothing is visible: it writes
 // zeros.
-__device__ __forceinline__ ExactSpan ex_seq_span(const ExactArgs &a, int n, int ql, int rs) {
+__device__ __forceinline__ ExactSpan ex_seq_span(const ExactArgs &a, int n, int ql, int rs, int wr) {
     ExactSpan s;
     const int tpt = ex_tpt(a.G);
     s.RT = (ql + tpt - 1) / tpt;
-    s.S = s.RT ? max(1, (ex_most_rows(a.window, a.sinks, tpt, n) + rs - 1) / rs) : 0;
+    s.S = s.RT ? max(1, (ex_most_rows(a.window, a.sinks, tpt, n, wr) + rs - 1) / rs) : 0;
     return s;
 }
 
 // By steps: length of the shared part of the space and of the first `seqs` sequences' part, by one
 // warp (every lane returns the sum).
-__device__ __forceinline__ unsigned ex_length(const ExactArgs &a, int seqs, int rs) {
+__device__ __forceinline__ unsigned ex_length(const ExactArgs &a, int seqs, int rs, int wr) {
     const int lane = threadIdx.x & 31;
     const ExactSpan p = ex_shared_span(a, rs);
     unsigned t = 0;
     if (!a.lens && !a.q_lens) {
-        const ExactSpan s = ex_seq_span(a, a.rows, a.m, rs);
+        const ExactSpan s = ex_seq_span(a, a.rows, a.m, rs, wr);
         t = (unsigned)seqs * a.H * s.RT * s.S;
     } else {
         for (int b = lane; b < seqs; b += 32) {
-            const ExactSpan s = ex_seq_span(a, ex_len(a, b), ex_qlen(a, b), rs);
+            const ExactSpan s = ex_seq_span(a, ex_len(a, b), ex_qlen(a, b), rs, wr);
             t += (unsigned)a.H * s.RT * s.S;
         }
         t = __reduce_add_sync(0xffffffffu, t);
@@ -121,9 +114,7 @@ __device__ __forceinline__ unsigned ex_length(const ExactArgs &a, int seqs, int 
     return t + (unsigned)a.H * p.RT * p.S;
 }
 
-// Warps per block of the split kernel, rows per warp and step.
-constexpr int EX_WARPS = 8;
-__host__ __device__ constexpr int ex_warp_rows(bool f32_rows) { return f32_rows ? 16 : 32; }
+constexpr int EX_WARPS = 8;            // warps per block of the split kernel
 
 cudaError_t launch_exact_split(const ExactArgs &a, const ExactMaps &maps, bool f32_rows, bool f32_io,
                                cudaStream_t s);

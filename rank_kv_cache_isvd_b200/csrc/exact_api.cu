@@ -315,7 +315,7 @@ void split_plan(ExactArgs &a, bool f32_rows, int sms) {
     const int tpt = ex_tpt(a.G), wr = ex_warp_rows(f32_rows);
     const int tiles = (a.m + tpt - 1) / tpt;
     const long long items = (long long)a.B * a.H * tiles;
-    const int most = ex_most_rows(a.window, a.sinks, tpt, a.rows);
+    const int most = ex_most_rows(a.window, a.sinks, tpt, a.rows, wr);
     a.cluster = 1;
     a.by_items = 0;
     a.rt_max = tiles;

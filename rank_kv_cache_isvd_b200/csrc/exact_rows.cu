@@ -48,20 +48,9 @@ exact_rows_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
     const int t0 = group * a.tq, t1 = min(t0 + a.tq, ql);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (t0 >= ql) return;
-    // the rows that the group sees, in an order without the gap between sinks and window: c < skp
-    // (sk of them, filled up to a multiple of 32) are the sinks, then the rows from lo on, up to C
-    int C = n, sk = 0, skp = 0, lo = 0;
-    if (!PREFIX) {
-        const int hi = max(0, n - ql + t1), s = min(a.sinks, hi), l = max(0, n - ql + t0 - a.window + 1);
-        C = hi;
-        if (l > s) {
-            sk = s;
-            skp = (s + 31) & ~31;
-            lo = l;
-            C = skp + hi - l;
-        }
-    }
-    const int steps = (C + WR - 1) / WR;
+    ExactOrder o = {n, 0, 0, 0};       // of the rows that the group sees
+    if (!PREFIX) o = ex_order(n, ql, t0, t1, a.window, a.sinks, WR);
+    const int steps = (o.C + WR - 1) / WR;
     const int s0 = (int)((long long)steps * sp / a.nsp), s1 = (int)((long long)steps * (sp + 1) / a.nsp);
     const int loads = 2 * (s1 - s0);
 
@@ -82,7 +71,7 @@ exact_rows_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
         if (issued >= RING) ok = wait_for(empty + at * 8, (issued / RING + 1) & 1);
         if (!ok) return false;
         if (lane == 0) {
-            const int c = (s0 + issued / 2) * WR, row = c < skp ? c : c - skp + lo;
+            const int row = ex_row(o, (s0 + issued / 2) * WR);
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full + at * 8),
                          "r"(UNIT)
                          : "memory");
@@ -113,8 +102,7 @@ exact_rows_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
 
     for (int u = 0; u < loads; u += 2) {
         const int c0 = (s0 + u / 2) * WR;
-        const bool sinks = c0 < skp;
-        const int seen = min(WR, (sinks ? sk : C) - c0), row0 = sinks ? c0 : c0 - skp + lo;
+        const int seen = ex_seen(o, c0, WR), row0 = ex_row(o, c0);
         const int ka = u % RING, va = (u + 1) % RING;
         late |= !wait_for(full + ka * 8, (u / RING) & 1);
         late |= !wait_for(full + va * 8, ((u + 1) / RING) & 1);

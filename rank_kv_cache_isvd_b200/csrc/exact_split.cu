@@ -62,39 +62,29 @@ __device__ __forceinline__ float4 ldc4(uint32_t a) {
     return f;
 }
 
-// Where an item's rows and queries are. Its visible rows in an order without the gap between sinks
-// and window: c < skp (sk of them, filled up to a multiple of 32) are the sinks, then the rows from
-// lo on, up to C.
+// Where an item's rows and queries are, and the order of its rows.
 struct Item {
     int b, h, rt;         // b < 0: shared prefix
     int n, ql;            // of sequence b
-    int C, sk, skp, lo;
+    ExactOrder o;
     int i0, i1;           // its tokens (sequences, for the shared prefix)
 };
 
+template <int WR>
 __device__ __forceinline__ void geometry(const ExactArgs &a, Item &it) {
     const int tpt = ex_tpt(a.G);
     it.i0 = it.rt * tpt;
-    it.sk = it.skp = it.lo = 0;
     if (it.b < 0) {
         it.i1 = min(it.i0 + tpt, a.B);
-        it.C = a.P;
+        it.o = {a.P, 0, 0, 0};
     } else {
         it.i1 = min(it.i0 + tpt, it.ql);
-        const int p0 = it.n - it.ql + it.i0;
-        const int hi = max(0, it.n - it.ql + it.i1);
-        const int sk = min(a.sinks, hi), lo = max(0, p0 - a.window + 1);
-        it.C = hi;
-        if (lo > sk) {
-            it.sk = sk;
-            it.skp = (sk + 31) & ~31;
-            it.lo = lo;
-            it.C = it.skp + hi - lo;
-        }
+        it.o = ex_order(it.n, it.ql, it.i0, it.i1, a.window, a.sinks, WR);
     }
 }
 
 // A way through a share of the work: the item, and the steps [s0, s1) of it to do.
+template <int WR>
 struct Walk {
     Item it;
     int s0, s1;
@@ -104,8 +94,8 @@ struct Walk {
 
     // -- by items: `rank` of `parts` blocks does its part of every item
     __device__ __forceinline__ void settle(const ExactArgs &a, int rs, int rank, int parts) {
-        geometry(a, it);
-        const unsigned n = (unsigned)max(1, (it.C + rs - 1) / rs);
+        geometry<WR>(a, it);
+        const unsigned n = (unsigned)max(1, (it.o.C + rs - 1) / rs);
         s0 = (int)(n * rank / parts);
         s1 = (int)(n * (rank + 1) / parts);
     }
@@ -160,7 +150,7 @@ struct Walk {
             it.n = it.ql = 0;
             at = 0;
         } else if (!a.lens && !a.q_lens) {
-            s = ex_seq_span(a, a.rows, a.m, rs);
+            s = ex_seq_span(a, a.rows, a.m, rs, WR);
             const unsigned each = (unsigned)a.H * s.RT * s.S;
             it.b = (int)((g - at) / each);
             at += it.b * each;
@@ -172,7 +162,7 @@ struct Walk {
                 const int b = b0 + lane;
                 unsigned len = 0;
                 if (b < a.B) {
-                    const ExactSpan x = ex_seq_span(a, ex_len(a, b), ex_qlen(a, b), rs);
+                    const ExactSpan x = ex_seq_span(a, ex_len(a, b), ex_qlen(a, b), rs, WR);
                     len = (unsigned)a.H * x.RT * x.S;
                 }
                 unsigned sum = len;
@@ -191,14 +181,14 @@ struct Walk {
                 at += __shfl_sync(0xffffffffu, sum, 31);
             }
             seq(a);
-            s = ex_seq_span(a, it.n, it.ql, rs);
+            s = ex_seq_span(a, it.n, it.ql, rs, WR);
         }
         S = s.S;
         const unsigned i = (g - at) / (unsigned)S;
         it.h = (int)(i / (unsigned)s.RT);
         it.rt = (int)(i - (unsigned)it.h * s.RT);
         first = at + i * S;
-        geometry(a, it);
+        geometry<WR>(a, it);
         cut();
     }
 
@@ -224,12 +214,12 @@ struct Walk {
                 do {
                     ++it.b;
                     seq(a);
-                    s = ex_seq_span(a, it.n, it.ql, rs);
+                    s = ex_seq_span(a, it.n, it.ql, rs, WR);
                 } while (s.S == 0 && it.b + 1 < a.B);
                 S = s.S;
             }
         }
-        geometry(a, it);
+        geometry<WR>(a, it);
         cut();
         return true;
     }
@@ -273,7 +263,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
         else if (T == 1) __syncwarp();
         else asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / T), "r"(32 * T) : "memory");
     };
-    Walk w;
+    Walk<WR> w;
     unsigned from, to;
     bool have;
     const unsigned my_team = (blockIdx.x / (unsigned)parts) * (EX_WARPS / T) + warp / T;
@@ -282,7 +272,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
         to = min(a.items, from + a.share + (my_team < a.extra ? 1u : 0u));
         have = w.begin(a, from, to, rs, rank, parts);
     } else {
-        const unsigned length = ex_length(a, a.B, rs);
+        const unsigned length = ex_length(a, a.B, rs, WR);
         const unsigned per = (length + a.teams - 1) / a.teams;
         from = my_team * per;
         to = min(length, from + per);
@@ -291,7 +281,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
     }
     bool late = false;                               // a wait hit its bound
     if (have) {
-        Walk nw = w;                                 // what is loaded next: nw's step `ns`, keys
+        Walk<WR> nw = w;                                 // what is loaded next: nw's step `ns`, keys
         int ns = nw.s0, loads = 0;                   // first (`loads` even), then values
         uint32_t ld_at = 0;
         bool more = true;
@@ -315,12 +305,12 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                 }
                 const Item &it = nw.it;
                 const int c0 = ns * rs + tw * WR;
-                if (c0 >= it.C) {
+                if (c0 >= it.o.C) {
                     ++ns;
                     continue;
                 }
                 if (lane == 0) {
-                    const int row = c0 < it.skp ? c0 : c0 - it.skp + it.lo;
+                    const int row = ex_row(it.o, c0);
                     const uint32_t b = bar + ld_at * 8;
                     const CUtensorMap *map = it.b < 0 ? (loads & 1 ? &maps.pv : &maps.pk)
                                                       : (loads & 1 ? &maps.v : &maps.k);
@@ -390,9 +380,8 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
 
             for (int st = w.s0; st < w.s1; ++st) {
                 const int c0 = st * rs + tw * WR;
-                if (c0 >= it.C) continue;
-                const bool sinks = c0 < it.skp;
-                const int seen = min(WR, (sinks ? it.sk : it.C) - c0);   // rows with a row behind
+                if (c0 >= it.o.C) continue;
+                const int seen = ex_seen(it.o, c0, WR);
                 late |= !wait_for(bar + unit * 8, parity);
                 float s[NT][2];                      // scores of row g at 8 nt + 2 t + x
                 x8.scores(ring + unit * UNIT, s);
@@ -402,7 +391,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
 #pragma unroll
                     for (int x = 0; x < 2; ++x) s[nt][x] *= a.scale_log2;
                 if (seen < WR || !plain) {
-                    const int row0 = sinks ? c0 : c0 - it.skp + it.lo;
+                    const int row0 = ex_row(it.o, c0);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -653,7 +642,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
             if (MASS && a.by_items) {
                 // the weights of the rows whose scores this team has
                 team_sync();
-                const int hi = min(it.C, w.s1 * rs);
+                const int hi = min(it.o.C, w.s1 * rs);
                 const float *sc = a.scores + ((long long)it.b * a.H + it.h) * a.G * a.score_st;
                 const long long base = ((long long)it.b * a.H + it.h) * a.rows;
                 // U groups of four rows per thread and turn, whose loads are in flight together;
@@ -727,7 +716,8 @@ constexpr int MERGE_CHUNK = 256;            // records whose weights are at hand
 template <bool F32ROWS, bool F32IO, bool MASS>
 __global__ void __launch_bounds__(MERGE_T)
 exact_merge_kernel(const __grid_constant__ ExactArgs a, int rt_max, int mass_blocks) {
-    const int RS = ex_warp_rows(F32ROWS) * a.team;
+    constexpr int WR = ex_warp_rows(F32ROWS);
+    const int RS = WR * a.team;
     __shared__ float wgt[EX_QROWS][MERGE_CHUNK];
     __shared__ float row_m[EX_QROWS], row_l[EX_QROWS];
     __shared__ __align__(16) float part[MERGE_T * 4];
@@ -747,11 +737,11 @@ exact_merge_kernel(const __grid_constant__ ExactArgs a, int rt_max, int mass_blo
         h = unit - b * a.H;
     }
     const int n = ex_len(a, b), ql = ex_qlen(a, b), tpt = ex_tpt(a.G);
-    const ExactSpan sp = ex_seq_span(a, n, ql, RS), sh = ex_shared_span(a, RS);
+    const ExactSpan sp = ex_seq_span(a, n, ql, RS, WR), sh = ex_shared_span(a, RS);
     if (rt >= sp.RT || (mass_block && chunk * MASS_ROWS >= n)) return;
-    const unsigned length = ex_length(a, a.B, RS);
+    const unsigned length = ex_length(a, a.B, RS, WR);
     const unsigned per = (length + a.teams - 1) / a.teams;
-    const unsigned first = ex_length(a, b, RS) + ((unsigned)h * sp.RT + rt) * sp.S;
+    const unsigned first = ex_length(a, b, RS, WR) + ((unsigned)h * sp.RT + rt) * sp.S;
     const int own_c0 = (int)(first / per), own_c1 = (int)((first + sp.S - 1) / per);
     const int n_own = own_c1 - own_c0 + 1;
     if (!MASS && !a.shared_here && !a.nsp && n_own == 1) return;   // the split kernel wrote it

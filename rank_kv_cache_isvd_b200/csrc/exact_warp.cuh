@@ -376,11 +376,11 @@ struct WarpRows {
         float x = l + __shfl_xor_sync(0xffffffffu, l, 1);
         return x + __shfl_xor_sync(0xffffffffu, x, 2);
     }
-    // Values of rows from `seen` on become zeros: rows that nobody sees may be anything, and
+    // Values of rows from `seen` (0 .. WR) on become zeros: rows that nobody sees may be anything, and
     // 0 x NaN would reach o. By the whole warp.
     static __device__ __forceinline__ void clear(uint32_t v, int seen) {
         const int lane = threadIdx.x & 31;
-        for (int r = seen; r < WR; ++r)
+        for (int r = max(seen, 0); r < WR; ++r)
             if (lane < 8 * PARTS)
                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
                                  v + (lane >> 3) * PART + r * 128 + (lane & 7) * 16),
