@@ -437,6 +437,16 @@ int iskv_prefix_decode_workspace(const iskv_exact_rows *rows, const iskv_exact_q
  */
 int iskv_exact_status(iskv_stream_t stream);
 
+/*
+ * Polls, of up to 20 us each, after which a device-side wait of the calls on exact caches gives up: for
+ * all calls of the process from now on, on all devices. ISKV_EXACT_POLLS (5 s) until it is called; 0: a wait
+ * gives up at once, which shows what a program does with the status. A call whose waits give up returns
+ * when its copies and products in flight have ended; what it has written is within its outputs.
+ * Errors: ISKV_ERR_INVALID_ARG (negative).
+ */
+#define ISKV_EXACT_POLLS (1 << 18)
+int iskv_exact_wait_limit(int polls);
+
 /* Static description of an error code. */
 const char *iskv_strerror(int code);
 

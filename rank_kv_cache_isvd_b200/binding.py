@@ -26,7 +26,7 @@ __all__ = [
     "iskv_exact_rows", "iskv_exact_queries", "iskv_exact_prefix",
     "iskv_window_attn", "iskv_window_attn_workspace", "iskv_mass_decode",
     "iskv_mass_decode_workspace", "iskv_evict", "iskv_evict_workspace", "iskv_prefix_decode",
-    "iskv_prefix_decode_workspace", "iskv_exact_status",
+    "iskv_prefix_decode_workspace", "iskv_exact_status", "iskv_exact_wait_limit", "ISKV_EXACT_POLLS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libiskv.so")
@@ -39,6 +39,7 @@ ISKV_ERR_NOT_CONVERGED = -4
 ISKV_ERR_NONFINITE = -5
 ISKV_ERR_UNSUPPORTED = -6
 ISKV_ERR_TIMEOUT = -7
+ISKV_EXACT_POLLS = 1 << 18
 ISKV_BF16 = 0
 ISKV_F32 = 1
 
@@ -193,6 +194,7 @@ _SIGNATURES = {
     "iskv_prefix_decode": (_i, [_vp, _vp, _vp, _vp, _sz, _vp]),
     "iskv_prefix_decode_workspace": (_i, [_vp, _vp, _vp, ctypes.POINTER(_sz)]),
     "iskv_exact_status": (_i, [_vp]),
+    "iskv_exact_wait_limit": (_i, [_i]),
 }
 
 
@@ -396,3 +398,7 @@ def iskv_prefix_decode_workspace(rows, q, prefix):
 
 def iskv_exact_status(stream=None) -> int:
     return lib.iskv_exact_status(_stream(stream))
+
+
+def iskv_exact_wait_limit(polls: int = ISKV_EXACT_POLLS) -> int:
+    return lib.iskv_exact_wait_limit(polls)

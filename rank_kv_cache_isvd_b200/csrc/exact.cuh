@@ -20,6 +20,8 @@ constexpr int EX_D = 128;
 constexpr int EX_QROWS = 8;            // query rows of a split-kernel tile (tokens x GQA group)
 constexpr int EX_REC = EX_QROWS * (2 + EX_D);   // floats of a record: m[8], l[8], O[8][128]
 constexpr int EX_PRE_MAX = 32;         // splits of a shared prefix at most
+// A device-side wait polls this often at most, each time suspended for up to so long (5 s in all).
+constexpr uint32_t EX_POLLS = ISKV_EXACT_POLLS, EX_SUSPEND_NS = 20000;
 
 struct ExactArgs {
     int B, H, rows;
@@ -49,6 +51,7 @@ struct ExactArgs {
     int cluster;                       // by items, team 8: blocks that share an item's steps
     int rt_max;                        // tiles per (sequence, kv-head) at most
     unsigned items, share, extra;      // by items: their number, and per team; `extra` teams take 1 more
+    uint32_t polls;                    // of a wait, before it gives up
     int after;                         // 1: launched next to the kernel before it, whose end it awaits
 };
 

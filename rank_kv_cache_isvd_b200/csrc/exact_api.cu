@@ -3,6 +3,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "evict.cuh"
@@ -37,6 +38,8 @@ int sm_count() {
     }
     return known[dev];
 }
+
+std::atomic<int> g_polls{(int)EX_POLLS};   // of a device-side wait, before it gives up
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -116,6 +119,7 @@ void fill(ExactArgs &a, const iskv_exact_rows *r, const iskv_exact_queries *q, i
     a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)EX_D));
     a.grid = sms;
     a.cluster = 1;
+    a.polls = (uint32_t)g_polls.load(std::memory_order_relaxed);
 }
 
 // Workspace of the split kernel: its teams' records, and with `items` one per item as well.
@@ -287,6 +291,7 @@ void tile_args(TileArgs &t, const TilePlan &p, const ExactArgs &a, bool prefix, 
     t.o_head = a.o_head;
     t.o_tok = a.o_tok;
     t.scale_log2 = a.scale_log2;
+    t.polls = a.polls;
     t.pre_ml = records;
     if (records)
         t.pre_o = reinterpret_cast<float *>(
@@ -585,6 +590,12 @@ extern "C" int iskv_evict(const iskv_exact_rows *r, const float *mass, float *ma
     a.keep = a.n_moves + units;
     a.moves = reinterpret_cast<int *>(static_cast<char *>(ws) + align256((size_t)units * 8));
     return launched(launch_evict(a, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int iskv_exact_wait_limit(int polls) {
+    if (polls < 0) return ISKV_ERR_INVALID_ARG;
+    g_polls.store(polls, std::memory_order_relaxed);
+    return ISKV_OK;
 }
 
 extern "C" int iskv_exact_status(iskv_stream_t stream) {

@@ -63,13 +63,15 @@ exact_rows_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
     }
     __syncthreads();
     int issued = 0;
+    bool late = false;                 // a wait of this lane gave up: it waits no more, and loads no more
     // Unit u (keys and values of a step in turn), by warp 0 once all warps are done with its place.
     auto load = [&]() {
-        if (issued >= loads) return true;
+        if (late || issued >= loads) return;
         const int at = issued % RING;
-        bool ok = true;
-        if (issued >= RING) ok = wait_for(empty + at * 8, (issued / RING + 1) & 1);
-        if (!ok) return false;
+        if (issued >= RING && !wait_for(empty + at * 8, (issued / RING + 1) & 1, a.polls)) {
+            late = true;
+            return;
+        }
         if (lane == 0) {
             const int row = ex_row(o, (s0 + issued / 2) * WR);
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full + at * 8),
@@ -79,11 +81,9 @@ exact_rows_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
                         b * a.seq_mul, full + at * 8);
         }
         ++issued;
-        return true;
     };
-    bool late = false;
     if (warp == 0)
-        for (int i = 0; i < RING; ++i) late |= !load();
+        for (int i = 0; i < RING; ++i) load();
 
     // this warp's tile of 8 rows
     const int tpt = ex_tpt(a.G);
@@ -104,8 +104,9 @@ exact_rows_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
         const int c0 = (s0 + u / 2) * WR;
         const int seen = ex_seen(o, c0, WR), row0 = ex_row(o, c0);
         const int ka = u % RING, va = (u + 1) % RING;
-        late |= !wait_for(full + ka * 8, (u / RING) & 1);
-        late |= !wait_for(full + va * 8, ((u + 1) / RING) & 1);
+        if (!late)
+            late = !wait_for(full + ka * 8, (u / RING) & 1, a.polls) ||
+                   !wait_for(full + va * 8, ((u + 1) / RING) & 1, a.polls);
         if (!PREFIX && seen < WR) {
             // values that no token of the group sees may be anything (the same steps in all warps)
             if (warp == 0) Rows::clear(ring + va * UNIT, seen);
@@ -143,8 +144,8 @@ exact_rows_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
             asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(empty + va * 8) : "memory");
         }
         if (warp == 0 && u >= LAG) {
-            late |= !load();
-            late |= !load();
+            load();
+            load();
         }
     }
 
@@ -172,11 +173,11 @@ exact_rows_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
         }
     }
     if (late) {
-        // copies still in flight end before the block does (bounded)
+        // copies still in flight end before the block does (bounded); the first lane has issued them
         atomicExch(&g_rows_status, 1);
-        if (warp == 0)
+        if (warp == 0 && lane == 0)
             for (int i = max(0, issued - RING); i < issued; ++i)
-                wait_for(full + (i % RING) * 8, (i / RING) & 1);
+                wait_for(full + (i % RING) * 8, (i / RING) & 1, EX_POLLS);
     }
 }
 

@@ -279,10 +279,14 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
         have = from < length;
         if (have) w.begin_steps(a, from, to, rs);
     }
-    bool late = false;                               // a wait hit its bound
+    // A wait of this lane gave up: it waits no more and, if it is the first lane, issues no more copies. The
+    // lanes do not agree on it (a vote behind every wait took 6 % of a call over float32 rows); they go
+    // through what is left of the steps, whose results say nothing then.
+    bool late = false;
     if (have) {
-        Walk<WR> nw = w;                                 // what is loaded next: nw's step `ns`, keys
+        Walk<WR> nw = w;                             // what is loaded next: nw's step `ns`, keys
         int ns = nw.s0, loads = 0;                   // first (`loads` even), then values
+        int armed = 0;                               // loads whose copies were issued
         uint32_t ld_at = 0;
         bool more = true;
         // Queries into L2, ahead of the rows' copies: they are read when the item begins.
@@ -309,7 +313,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                     ++ns;
                     continue;
                 }
-                if (lane == 0) {
+                if (lane == 0 && !late) {
                     const int row = ex_row(it.o, c0);
                     const uint32_t b = bar + ld_at * 8;
                     const CUtensorMap *map = it.b < 0 ? (loads & 1 ? &maps.pv : &maps.pk)
@@ -323,6 +327,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                 }
                 ns += loads & 1;
                 ++loads;
+                if (!late) armed = loads;
                 ld_at = ld_at + 1 == UNITS ? 0 : ld_at + 1;
                 return;
             }
@@ -334,6 +339,9 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
         Rows x8;
         x8.init();
         uint32_t unit = 0, parity = 0;
+        auto full = [&]() {                          // the unit in use has arrived
+            if (!wait_for(bar + unit * 8, parity, late ? 0u : a.polls)) late = true;
+        };
         auto taken = [&]() {                         // the unit in use is free: refill it
             __syncwarp();
             load();
@@ -382,7 +390,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                 const int c0 = st * rs + tw * WR;
                 if (c0 >= it.o.C) continue;
                 const int seen = ex_seen(it.o, c0, WR);
-                late |= !wait_for(bar + unit * 8, parity);
+                full();
                 float s[NT][2];                      // scores of row g at 8 nt + 2 t + x
                 x8.scores(ring + unit * UNIT, s);
                 taken();
@@ -412,7 +420,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                     }
                 }
                 x8.weights(s);
-                late |= !wait_for(bar + unit * 8, parity);
+                full();
                 if (seen < WR) Rows::clear(ring + unit * UNIT, seen);
                 x8.values(ring + unit * UNIT);
                 taken();
@@ -696,10 +704,10 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
             have = w.next(a, rs, rank, parts);
         }
         if (late) {
-            // copies still in flight end before the block does (bounded)
+            // copies still in flight end before the block does (bounded); the first lane has issued them
             atomicExch(&g_split_status, 1);
-            for (int i = max(0, loads - UNITS); i < loads; ++i)
-                wait_for(bar + (i % UNITS) * 8, (i / UNITS) & 1);
+            for (int i = max(0, armed - UNITS); lane == 0 && i < armed; ++i)
+                wait_for(bar + (i % UNITS) * 8, (i / UNITS) & 1, EX_POLLS);
         }
     }
     // the merge waits for this kernel alone: it must not end before the one that ran beside it

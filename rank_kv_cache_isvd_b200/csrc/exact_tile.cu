@@ -28,7 +28,7 @@
 // P is rounded to bf16 (half a step, up to 2^-8 of a weight, at random over the keys);
 // the sum l takes the unrounded values, and all sums are float32.
 //
-// Every wait is bounded. A wait that gives up sets the CTA's abort flag and the device's status
+// Every wait is bounded (iskv_exact_wait_limit). A wait that gives up sets the CTA's abort flag and the device's status
 // word; all roles then leave their loops, copies in flight are waited for, and tensor memory is
 // freed.
 #include <math_constants.h>
@@ -46,7 +46,6 @@ constexpr int TT = 384;
 constexpr int NSTAGE = 5;
 constexpr int BLOCK_BYTES = 128 * 256;       // 128 rows of 128 bf16: two halves of 64 channels
 constexpr int HALF_BYTES = 128 * 128;
-constexpr uint32_t POLLS = 1u << 18, SUSPEND_NS = 20000;
 
 // setmaxnreg: 128 control threads and 256 softmax threads share what the launch was given
 constexpr int REG_LO = 72, REG_HI = 216, REG_LAUNCH = 168;
@@ -61,16 +60,17 @@ struct Bars {
 };
 constexpr size_t TILE_SMEM = 2 * BLOCK_BYTES + NSTAGE * BLOCK_BYTES + sizeof(Bars) + 1024;
 
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort) {
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, uint32_t polls,
+                                         volatile int *abort) {
     const uint32_t a = smem_u32(bar);
-    for (uint32_t i = 0; i < POLLS; ++i) {
+    for (uint32_t i = 0; i < polls; ++i) {
         uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done)
-            : "r"(a), "r"(parity), "r"(SUSPEND_NS)
+            : "r"(a), "r"(parity), "r"(EX_SUSPEND_NS)
             : "memory");
         if (done) return true;
         if (*abort) return false;
@@ -307,7 +307,7 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ Ti
             auto load = [&](const CUtensorMap *map, const CUtensorMap *map16, int blk) {
                 const int st = issued % NSTAGE;
                 if (issued >= NSTAGE &&
-                    !wait_bar(&bars->kv_empty[st], (issued / NSTAGE + 1) & 1, abort_flag))
+                    !wait_bar(&bars->kv_empty[st], (issued / NSTAGE + 1) & 1, a.polls, abort_flag))
                     return false;
                 const int c = w.base(blk), hd = w.h * a.head_mul, sq = w.b * a.seq_mul;
                 uint8_t *dst = ring + st * BLOCK_BYTES;
@@ -339,7 +339,7 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ Ti
         int st = 0;                                    // stage of the ring to take next
         uint32_t phase = 0;
         auto wait = [&](uint64_t *bar, uint32_t parity) {   // the same answer in every lane
-            return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag)) != 0;
+            return __all_sync(0xffffffffu, wait_bar(bar, parity, a.polls, abort_flag)) != 0;
         };
         auto full = [&]() { return wait(&bars->kv_full[st], phase); };
         auto qk = [&](int i, uint32_t k) {              // S_i = Q_i K^T
@@ -475,7 +475,7 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ Ti
         float2 l2 = make_float2(0.f, 0.f);
         bool ok = true;
         for (int x = 0; x < mine; ++x) {
-            ok = wait_bar(&bars->s_full[i], x & 1, abort_flag);
+            ok = wait_bar(&bars->s_full[i], x & 1, a.polls, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -555,7 +555,7 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ Ti
         // ---- the tile is complete: out = O / l, or a record of this split -----------------------
         const float l = l2.x + l2.y;
         if (N > 0 && ok) {
-            ok = wait_bar(&bars->o_full, 0, abort_flag);
+            ok = wait_bar(&bars->o_full, 0, a.polls, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
         }
@@ -658,10 +658,15 @@ exact_tile_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ Ti
         // products and copies in flight end before the block does (bounded waits)
         atomicExch(&g_tile_status, 1);
         if (N > 0) {
-            bool late = !mbar_wait(&bars->o_full, 0) | !mbar_wait(&bars->q_full, 0);
+            int unset;
+            auto drain = [&](uint64_t *bar, uint32_t parity) {
+                unset = 0;
+                wait_bar(bar, parity, EX_POLLS, &unset);
+            };
+            drain(&bars->o_full, 0);
+            drain(&bars->q_full, 0);
             for (int i = max(0, bars->issued - NSTAGE); i < bars->issued; ++i)
-                late |= !mbar_wait(&bars->kv_full[i % NSTAGE], (i / NSTAGE) & 1);
-            (void)late;
+                drain(&bars->kv_full[i % NSTAGE], (i / NSTAGE) & 1);
         }
     }
     __syncthreads();

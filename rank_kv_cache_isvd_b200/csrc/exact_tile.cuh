@@ -26,6 +26,7 @@ struct TileArgs {
     float *pre_ml, *pre_o;             // ... or records [B H][nsp][m G][2] and [..][128]
                                        // (prefix: [H][nsp][sequences G])
     float scale_log2;
+    unsigned polls;                    // of a wait, before it gives up
 };
 
 // Maps of q (channels, q-heads, tokens, sequences) in boxes of 64 channels; of the rows (64 channels,

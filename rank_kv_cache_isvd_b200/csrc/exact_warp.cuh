@@ -26,7 +26,6 @@
 namespace iskv {
 
 constexpr int UNIT = 8192;             // bytes of keys or values per warp and step
-constexpr uint32_t EX_POLLS = 1u << 18, EX_SUSPEND_NS = 20000;
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -136,8 +135,9 @@ __device__ __forceinline__ void tma_load_5d_once(uint32_t dst, const CUtensorMap
         "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(0), "r"(head), "r"(seq), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
-    for (uint32_t i = 0; i < EX_POLLS; ++i) {
+// False: the wait gave up.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, uint32_t polls) {
+    for (uint32_t i = 0; i < polls; ++i) {
         uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"

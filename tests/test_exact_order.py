@@ -86,3 +86,9 @@ def test_steps_have_rows_and_cover_what_is_seen(tmp_path):
     subprocess.run([cxx, "-O2", "-std=c++17", "-I", CSRC, str(src), "-o", str(exe)], check=True)
     run = subprocess.run([str(exe)], capture_output=True, text=True)
     assert run.returncode == 0, run.stdout
+
+
+def test_wait_limits_are_checked():
+    import rank_kv_cache_isvd_b200 as iskv
+    assert iskv.iskv_exact_wait_limit(-1) == iskv.ISKV_ERR_INVALID_ARG
+    assert iskv.iskv_exact_wait_limit(1) == 0 and iskv.iskv_exact_wait_limit() == 0
