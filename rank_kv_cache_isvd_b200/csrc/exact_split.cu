@@ -504,6 +504,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                 }
                 if (finish && parts == 1) {
                     write(it, r, y, L);
+                    if (MASS) __syncwarp();          // every lane has read the row's references and sums
                     if (MASS && lane == 0) {
                         // (reference, sum) of the row for the weights below
                         red_m[team0 * EX_QROWS + r] = ref;
