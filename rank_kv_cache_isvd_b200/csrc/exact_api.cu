@@ -83,12 +83,16 @@ int check_queries(const iskv_exact_rows *r, const iskv_exact_queries *q) {
         return ISKV_ERR_INVALID_ARG;
     // float32 rows go with float32 queries and outputs
     if (r->dtype == ISKV_F32 && q->dtype != ISKV_F32) return ISKV_ERR_UNSUPPORTED;
-    // (tile, step) pairs are counted in 32 bits
-    const long long tiles = (q->m + ex_tpt(q->n_q_heads / r->n_kv_heads) - 1) /
-                            ex_tpt(q->n_q_heads / r->n_kv_heads);
-    if ((long long)r->batch * r->n_kv_heads * tiles * (r->rows / 16 + 3) > 0x7fffffffLL)
-        return ISKV_ERR_UNSUPPORTED;
     return ISKV_OK;
+}
+
+// The split kernel counts (tile, step) pairs in 32 bits.
+int check_split(const iskv_exact_rows *r, const iskv_exact_queries *q) {
+    const int tpt = ex_tpt(q->n_q_heads / r->n_kv_heads);
+    const long long tiles = (q->m + tpt - 1) / tpt;
+    return (long long)r->batch * r->n_kv_heads * tiles * (r->rows / 16 + 3) > 0x7fffffffLL
+               ? ISKV_ERR_UNSUPPORTED
+               : ISKV_OK;
 }
 
 // 0 where the items of a dimension all sit in one place: maps then have an extent of 1 there.
@@ -219,12 +223,17 @@ struct TilePlan {
     int tq, pairs, nsp;
 };
 
+// Whether a call takes the kernels for many query rows. One tile of 8 reads the rows once in the split kernel
+// as well.
+bool many_rows(int tokens, int G, long long seen) {
+    return tokens * (long long)G > EX_QROWS && seen > 0;
+}
+
 // `tokens` query tokens (prefix: sequences) per unit, over at most `seen` rows each.
 TilePlan tile_plan(int units, int tokens, int G, long long seen, bool tile, int sms) {
     TilePlan p;
     memset(&p, 0, sizeof(p));
-    // one tile of 8 query rows reads the rows once in the split kernel as well
-    p.use = tokens * (long long)G > EX_QROWS && seen > 0;
+    p.use = many_rows(tokens, G, seen);
     if (!p.use) return p;
     p.tile = tile;
     p.tq = tile ? TILE_ROWS / G : EX_WARPS * ex_tpt(G);
@@ -384,10 +393,17 @@ extern "C" int iskv_window_attn_workspace(const iskv_exact_rows *r, const iskv_e
     int rc = check_rows(r);
     if (rc == ISKV_OK) rc = check_queries(r, q);
     if (rc != ISKV_OK) return rc;
-    const int sms = sm_count();
-    if (!sms) return ISKV_ERR_CUDA;
     const long long units = (long long)r->batch * r->n_kv_heads;
     const int G = q->n_q_heads / r->n_kv_heads;
+    if (!many_rows(q->m, G, r->rows)) rc = check_split(r, q);
+    if (rc != ISKV_OK) return rc;
+    // a grid's blocks (the rows are split only where they are fewer than the SMs)
+    for (int tile = 0; tile <= (all_bf16(r, q) ? 1 : 0); ++tile) {
+        const TilePlan p = window_plan(r, q, window, sinks, tile != 0, 1);
+        if (p.use && units * p.pairs > 0x7fffffffLL) return ISKV_ERR_UNSUPPORTED;
+    }
+    const int sms = sm_count();
+    if (!sms) return ISKV_ERR_CUDA;
     *bytes = record_bytes(sms, 0);
     // what the call takes: queries that cannot be mapped go to the rows kernel
     for (int tile = 0; tile <= (all_bf16(r, q) ? 1 : 0); ++tile) {
@@ -436,6 +452,7 @@ extern "C" int iskv_mass_decode_workspace(const iskv_exact_rows *r, const iskv_e
     if (!bytes) return ISKV_ERR_INVALID_ARG;
     int rc = check_rows(r);
     if (rc == ISKV_OK) rc = check_queries(r, q);
+    if (rc == ISKV_OK) rc = check_split(r, q);
     if (rc != ISKV_OK) return rc;
     if (q->m != 1 || q->q_lens) return ISKV_ERR_INVALID_ARG;
     const int sms = sm_count();
@@ -471,6 +488,7 @@ extern "C" int iskv_prefix_decode_workspace(const iskv_exact_rows *r, const iskv
     if (!bytes || !p) return ISKV_ERR_INVALID_ARG;
     int rc = check_rows(r);
     if (rc == ISKV_OK) rc = check_queries(r, q);
+    if (rc == ISKV_OK) rc = check_split(r, q);
     if (rc != ISKV_OK) return rc;
     const int e = esz_of(r->dtype);
     if (q->m != 1 || q->q_lens || p->rows < 0 || p->rows > kMaxRows ||
