@@ -21,9 +21,54 @@ def _strides(x: torch.Tensor, n: int):
     return [s if e > 1 else 0 for s, e in zip(x.stride()[:n], x.shape[:n])]
 
 
+def _span(x: torch.Tensor) -> int:
+    """Bytes from the first element of ``x`` to behind its last one."""
+    return x.element_size() * (1 + sum((e - 1) * s for s, e in zip(x.stride(), x.shape))) if x.numel() else 0
+
+
+def _overlap(delta: int, a, b, row: int) -> bool:
+    """Whether two tensors of rows of ``row`` bytes share a byte: the second begins ``delta`` bytes behind the
+    first; ``a``, ``b``: their rows' ``(stride in bytes, extent)``. Looks for places i, j with
+    ``|delta + j . b - i . a| < row``, the longest stride first. A search that grows long (tensors whose
+    dimensions do not nest) counts as an overlap."""
+    reach: dict = {}                                 # stride: range of its factor
+    for strides, low, high in ((a, 0, 1), (b, -1, 0)):
+        for s, e in strides:
+            if s > 0 and e > 1:
+                x = reach.get(s, (0, 0))
+                reach[s] = (x[0] + low * (e - 1), x[1] + high * (e - 1))
+    dims = sorted(((s, lo, hi) for s, (lo, hi) in reach.items()), reverse=True)
+    low, high = [0], [0]                             # sums of the dimensions behind
+    for s, lo, hi in reversed(dims):
+        low.append(low[-1] + s * lo)
+        high.append(high[-1] + s * hi)
+    low.reverse()
+    high.reverse()
+    left, steps = [(0, delta)], 0
+    while left:
+        i, d = left.pop()
+        if i == len(dims):
+            if abs(d) < row:
+                return True
+            continue
+        s, lo, hi = dims[i]
+        first = max(lo, -((row - 1 + high[i + 1] - d) // s))         # d - x s <= high + row - 1
+        last = min(hi, (d - low[i + 1] + row - 1) // s)              # d - x s >= low - row + 1
+        steps += max(0, last - first + 1)
+        if steps > 10000:
+            return True
+        left.extend((i + 1, d - x * s) for x in range(first, last + 1))
+    return False
+
+
+def _rows_of(x: torch.Tensor):
+    return [(s * x.element_size(), e) for s, e in zip(x.stride()[:-1], x.shape[:-1])]
+
+
 class _Plan:
-    """What a form of a call keeps: its C structs, their addresses, and its workspace's size."""
-    __slots__ = ("x", "x_at", "p", "p_at", "need")
+    """What a form of a call keeps: its C structs, their addresses, the spans of queries and outputs, and
+    its workspace's size."""
+    __slots__ = ("x", "x_at", "p", "p_at", "need", "q_span", "out_span")
 
 
 class ExactKVCache:
@@ -56,6 +101,7 @@ class ExactKVCache:
         self.batch, self.n_kv_heads, self.rows = k.shape[:3]
         self._batch_shape = torch.Size((self.batch,))
         self._mass_shape = torch.Size((self.batch, self.n_kv_heads, self.rows))
+        self._mass_bytes = 4 * self._mass_shape.numel()
         if lens is not None:
             self._check(lens, "lens", torch.int32, self._batch_shape)
         self._rows = iskv_exact_rows(k.data_ptr(), v.data_ptr(), *_strides(k, 3), *k.shape[:3],
@@ -124,15 +170,23 @@ class ExactKVCache:
                                     *(_strides(out, dims - 1) + rest), q.shape[1],
                                     q.shape[2] if tokens else 1, _TYPES[q.dtype], None)
         plan.x_at = ctypes.addressof(plan.x)
+        plan.q_span, plan.out_span = _span(q), _span(out)
 
     @staticmethod
-    def _apart(q: torch.Tensor, out: torch.Tensor):
+    def _apart(plan, q: torch.Tensor, out: torch.Tensor):
         """Addresses of queries and outputs. Blocks that share queries read them at different times,
-        so outputs cannot take their place."""
+        so outputs cannot take the place of any."""
         at, to = q.data_ptr(), out.data_ptr()
-        if at == to and q.numel():
-            raise ValueError("out must not be q")
+        if at < to + plan.out_span and to < at + plan.q_span and _overlap(
+                to - at, _rows_of(q), _rows_of(out), D * q.element_size()):
+            raise ValueError("out must not overlap q")
         return at, to
+
+    @staticmethod
+    def _in_place(at: int, to: int, size: int, what: str) -> None:
+        """Of contiguous arrays of ``size`` bytes: the one at ``to`` is the one at ``at``, or apart."""
+        if at != to and -size < to - at < size:
+            raise ValueError(f"{what} must be the input or not overlap it")
 
     def _on_device(self, *tensors) -> None:
         for x in tensors:
@@ -170,7 +224,7 @@ class ExactKVCache:
                            out.dtype, window, sinks), make)
         self._on_device(q, out)
         x, ws = plan.x, self._ws
-        x.q, x.out = self._apart(q, out)
+        x.q, x.out = self._apart(plan, q, out)
         x.q_lens = None
         if q_lens is not None:
             self._check(q_lens, "q_lens", torch.int32, self._batch_shape)
@@ -195,6 +249,7 @@ class ExactKVCache:
             mass_out = mass
         else:
             self._check(mass_out, "mass_out", torch.float32, self._mass_shape)
+            self._in_place(mass.data_ptr(), mass_out.data_ptr(), self._mass_bytes, "mass_out")
         if out is None:
             out = torch.empty_like(q)
 
@@ -206,7 +261,7 @@ class ExactKVCache:
                            out.dtype), make)
         self._on_device(q, out)
         x, ws = plan.x, self._ws
-        x.q, x.out = self._apart(q, out)
+        x.q, x.out = self._apart(plan, q, out)
         s = self._stream()
         self._call("iskv_mass_decode", lib.iskv_mass_decode, self._rows_at, plan.x_at,
                    mass.data_ptr(), mass_out.data_ptr(), ws.data_ptr(), plan.need, s)
@@ -238,11 +293,16 @@ class ExactKVCache:
         if pos_out is not pos:
             self._check(pos_out, "pos_out", torch.int32, shape)
         self._check(lens_out, "lens_out", torch.int32, self._batch_shape)
+        m, m_to, p, p_to = mass.data_ptr(), mass_out.data_ptr(), pos.data_ptr(), pos_out.data_ptr()
+        l_to = lens_out.data_ptr()
+        self._in_place(m, m_to, self._mass_bytes, "mass_out")
+        self._in_place(p, p_to, self._mass_bytes, "pos_out")
+        if self._rows.lens:
+            self._in_place(self._rows.lens, l_to, 4 * self.batch, "lens_out")
         plan = self._plan(("iskv_evict", budget), lambda _: iskv_evict_workspace(self._rows, budget))
         ws = self._ws
-        self._call("iskv_evict", lib.iskv_evict, self._rows_at, mass.data_ptr(), mass_out.data_ptr(),
-                   pos.data_ptr(), pos_out.data_ptr(), lens_out.data_ptr(), budget, recent, sinks,
-                   ws.data_ptr(), plan.need, self._stream())
+        self._call("iskv_evict", lib.iskv_evict, self._rows_at, m, m_to, p, p_to, l_to, budget, recent,
+                   sinks, ws.data_ptr(), plan.need, self._stream())
 
     def prefix_decode(self, q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Tensor, *,
                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -273,7 +333,7 @@ class ExactKVCache:
                            prefix_v.stride(), prefix_k.dtype, prefix_v.dtype), make)
         self._on_device(q, out, prefix_k, prefix_v)
         x, p, ws = plan.x, plan.p, self._ws
-        x.q, x.out = self._apart(q, out)
+        x.q, x.out = self._apart(plan, q, out)
         p.k, p.v = prefix_k.data_ptr(), prefix_v.data_ptr()
         s = self._stream()
         self._call("iskv_prefix_decode", lib.iskv_prefix_decode, self._rows_at, plan.x_at, plan.p_at,
