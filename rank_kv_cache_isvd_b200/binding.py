@@ -346,7 +346,16 @@ def _ref(x):
     return None if x is None else ctypes.addressof(x)
 
 
+def _int32(**numbers):
+    """The numbers, which C takes in 32 bits: others would lose their upper ones on the way."""
+    for what, x in numbers.items():
+        if not -1 << 31 <= x < 1 << 31:
+            raise ValueError(f"{what} must fit in 32 bits")
+    return tuple(numbers.values())
+
+
 def iskv_window_attn(rows, q, window: int, sinks: int, ws, ws_bytes: int, stream=None) -> int:
+    window, sinks = _int32(window=window, sinks=sinks)
     return lib.iskv_window_attn(_ref(rows), _ref(q), window, sinks, _ptr(ws), ws_bytes,
                                 _stream(stream))
 
@@ -354,6 +363,7 @@ def iskv_window_attn(rows, q, window: int, sinks: int, ws, ws_bytes: int, stream
 def iskv_window_attn_workspace(rows, q, window: int, sinks: int):
     """Returns ``(code, bytes)``."""
     n = _sz(0)
+    window, sinks = _int32(window=window, sinks=sinks)
     code = lib.iskv_window_attn_workspace(_ref(rows), _ref(q), window, sinks, ctypes.byref(n))
     return code, n.value
 
@@ -372,6 +382,7 @@ def iskv_mass_decode_workspace(rows, q):
 
 def iskv_evict(rows, mass, mass_out, pos, pos_out, lens_out, budget: int, recent: int, sinks: int,
                ws, ws_bytes: int, stream=None) -> int:
+    budget, recent, sinks = _int32(budget=budget, recent=recent, sinks=sinks)
     return lib.iskv_evict(_ref(rows), _ptr(mass), _ptr(mass_out), _ptr(pos), _ptr(pos_out),
                           _ptr(lens_out), budget, recent, sinks, _ptr(ws), ws_bytes,
                           _stream(stream))
@@ -380,6 +391,7 @@ def iskv_evict(rows, mass, mass_out, pos, pos_out, lens_out, budget: int, recent
 def iskv_evict_workspace(rows, budget: int):
     """Returns ``(code, bytes)``."""
     n = _sz(0)
+    (budget,) = _int32(budget=budget)
     code = lib.iskv_evict_workspace(_ref(rows), budget, ctypes.byref(n))
     return code, n.value
 
@@ -401,4 +413,4 @@ def iskv_exact_status(stream=None) -> int:
 
 
 def iskv_exact_wait_limit(polls: int = ISKV_EXACT_POLLS) -> int:
-    return lib.iskv_exact_wait_limit(polls)
+    return lib.iskv_exact_wait_limit(*_int32(polls=polls))

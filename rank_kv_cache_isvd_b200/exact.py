@@ -7,7 +7,7 @@ import ctypes
 
 import torch
 
-from .binding import (ISKV_BF16, ISKV_F32, check, iskv_evict_workspace, iskv_exact_prefix,
+from .binding import (ISKV_BF16, ISKV_F32, _int32, check, iskv_evict_workspace, iskv_exact_prefix,
                       iskv_exact_queries, iskv_exact_rows, iskv_exact_status,
                       iskv_mass_decode_workspace, iskv_prefix_decode_workspace,
                       iskv_window_attn_workspace, lib)
@@ -299,7 +299,11 @@ class ExactKVCache:
         self._in_place(p, p_to, self._mass_bytes, "pos_out")
         if self._rows.lens:
             self._in_place(self._rows.lens, l_to, 4 * self.batch, "lens_out")
-        plan = self._plan(("iskv_evict", budget), lambda _: iskv_evict_workspace(self._rows, budget))
+        def make(plan):
+            _int32(recent=recent, sinks=sinks)
+            return iskv_evict_workspace(self._rows, budget)
+
+        plan = self._plan(("iskv_evict", budget, recent, sinks), make)
         ws = self._ws
         self._call("iskv_evict", lib.iskv_evict, self._rows_at, m, m_to, p, p_to, l_to, budget, recent,
                    sinks, ws.data_ptr(), plan.need, self._stream())
