@@ -110,7 +110,8 @@ class ExactKVCache:
         self._plans: dict = {}          # per form of a call: its structs and workspace size
         self._ws: torch.Tensor | None = None
         self._ws_stream = 0             # whose memory it is
-        self._old_ws: list = []         # captured graphs may hold their addresses
+        self._ws_captured = False       # a graph may hold its address
+        self._old_ws: list = []         # earlier ones of which that is true
 
     # -- plumbing --------------------------------------------------------------------------------
     def _check(self, x: torch.Tensor, what: str, dtype, shape) -> None:
@@ -130,8 +131,15 @@ class ExactKVCache:
         return torch.cuda.stream(stream)
 
     def _stream(self) -> int:
-        """The current stream; the workspace is not handed out before its work on it is done."""
+        """The current stream; the workspace is not handed out before its work on it is done, nor while
+        a graph that is captured now may use it."""
         raw = torch._C._cuda_getCurrentRawStream(self._index)
+        if not self._ws_captured and raw:            # (the default stream cannot be captured)
+            if torch._C._cuda_getDevice() == self._index:
+                self._ws_captured = torch._C._cuda_isCurrentStreamCapturing()
+            else:
+                with torch.cuda.device(self._index):
+                    self._ws_captured = torch._C._cuda_isCurrentStreamCapturing()
         if raw != self._ws_stream:
             self._ws.record_stream(torch.cuda.current_stream(self.device))
         return raw
@@ -148,10 +156,16 @@ class ExactKVCache:
                 self._plans.clear()
             self._plans[key] = plan
         if self._ws is None or self._ws.numel() < plan.need:
+            size = plan.need
             if self._ws is not None:
-                self._old_ws.append(self._ws)
-            self._ws = torch.empty((plan.need,), dtype=torch.uint8, device=self.device)
+                # half as large again at least: forms that grow call by call ask for few, and those that
+                # graphs keep add up to three times the largest
+                size = max(size, self._ws.numel() * 3 // 2)
+                if self._ws_captured:
+                    self._old_ws.append(self._ws)
+            self._ws = torch.empty((size,), dtype=torch.uint8, device=self.device)
             self._ws_stream = torch._C._cuda_getCurrentRawStream(self._index)
+            self._ws_captured = False
         return plan
 
     def _queries(self, plan, q: torch.Tensor, out: torch.Tensor, tokens: bool):
