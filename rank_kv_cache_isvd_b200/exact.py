@@ -76,8 +76,8 @@ class ExactKVCache:
     tensors (bf16 or float32, the same strides, last dimension contiguous; any order of the others,
     so a view of ``[batch][rows][n_kv][128]`` is fine), attended as they are (keys already
     rotated). ``lens``: int32 ``[batch]`` on the device, the rows that each sequence holds;
-    ``None``: all. The tensors are read at each call: rows written and lengths advanced between
-    calls count.
+    ``None``: all. The tensors are read at each call: rows written and lengths advanced in place
+    between calls count; other tensors need another object.
 
     Calls run on the current stream of the tensors' device, or as if ``stream`` were that one, and
     synchronise nothing. They share the object's workspace: calls that may overlap (other streams, graphs
@@ -95,7 +95,7 @@ class ExactKVCache:
             raise ValueError("k and v must both be bfloat16 or float32")
         if k.stride(-1) != 1 or v.stride(-1) != 1 or _strides(k, 3) != _strides(v, 3):
             raise ValueError("k and v must have the same strides and contiguous rows")
-        self.k, self.v, self.lens = k, v, lens
+        self._k, self._v, self._lens = k, v, lens
         self.device = k.device
         self._index = k.get_device()
         self.batch, self.n_kv_heads, self.rows = k.shape[:3]
@@ -112,6 +112,19 @@ class ExactKVCache:
         self._ws_stream = 0             # whose memory it is
         self._ws_captured = False       # a graph may hold its address
         self._old_ws: list = []         # earlier ones of which that is true
+
+    # The C structs hold their addresses: they cannot be replaced.
+    @property
+    def k(self) -> torch.Tensor:
+        return self._k
+
+    @property
+    def v(self) -> torch.Tensor:
+        return self._v
+
+    @property
+    def lens(self) -> torch.Tensor | None:
+        return self._lens
 
     # -- plumbing --------------------------------------------------------------------------------
     def _check(self, x: torch.Tensor, what: str, dtype, shape) -> None:
@@ -296,7 +309,7 @@ class ExactKVCache:
                                   mass_out=mass_out, pos_out=pos_out, lens_out=lens_out)
         mass_out = mass if mass_out is None else mass_out
         pos_out = pos if pos_out is None else pos_out
-        lens_out = self.lens if lens_out is None else lens_out
+        lens_out = self._lens if lens_out is None else lens_out
         if lens_out is None:
             raise ValueError("a cache without lens needs lens_out")
         shape = self._mass_shape
@@ -335,7 +348,7 @@ class ExactKVCache:
         def make(plan):
             for x in (prefix_k, prefix_v):
                 if (x.dim() != 3 or x.shape[0] != self.n_kv_heads or x.shape[-1] != D or
-                        x.dtype != self.k.dtype or x.device != self.device or x.stride(-1) != 1):
+                        x.dtype != self._k.dtype or x.device != self.device or x.stride(-1) != 1):
                     raise ValueError("prefix_k and prefix_v must be [n_kv][P][128], in the rows' "
                                      "dtype and on their device, with contiguous rows")
             if prefix_k.shape != prefix_v.shape or _strides(prefix_k, 2) != _strides(prefix_v, 2):

@@ -63,3 +63,9 @@ def test_random_views(seed):
         seen[want] += 1
         assert _shares(q, out) == want, (q.stride(), q.shape, out.stride(), out.shape)
     assert min(seen.values()) > 40
+
+
+def test_tensors_are_read_only():
+    from rank_kv_cache_isvd_b200 import ExactKVCache
+    for name in ("k", "v", "lens"):
+        assert getattr(ExactKVCache, name).fset is None

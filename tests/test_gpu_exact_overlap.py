@@ -60,3 +60,14 @@ def test_arrays_that_overlap_in_part_are_refused():
     other = ExactKVCache(cache.k, cache.v, lens=lens[:2])
     with pytest.raises(ValueError):
         other.evict(m0, p0, budget=100, recent=10, lens_out=lens[1:])
+
+
+def test_tensors_of_an_object_cannot_be_replaced():
+    """The C structs hold their addresses, so ``cache.lens = cache.lens + 1`` would go on reading what the old
+    tensor held, or what is there when it is gone."""
+    cache, _ = _cache()
+    for name in ("k", "v", "lens"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, getattr(cache, name).clone())
+    cache.lens.sub_(1)                                       # in place: the object sees it
+    assert cache.lens.tolist() == [199, 199]
