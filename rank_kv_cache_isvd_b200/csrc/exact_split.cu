@@ -279,14 +279,14 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
         have = from < length;
         if (have) w.begin_steps(a, from, to, rs);
     }
-    // A wait of this lane gave up: it waits no more and, if it is the first lane, issues no more copies. The
-    // lanes do not agree on it (a vote behind every wait took 6 % of a call over float32 rows); they go
-    // through what is left of the steps, whose results say nothing then.
-    bool late = false;
+    // Once a wait of this lane has given up: how many loads were issued then (-1 before). It waits no more
+    // and, if it is the first lane, issues no more copies. The lanes do not agree on it (a vote behind every
+    // wait took 6 % of a call over float32 rows); they go through what is left of the steps, whose results
+    // say nothing then.
+    int late = -1;
     if (have) {
         Walk<WR> nw = w;                             // what is loaded next: nw's step `ns`, keys
         int ns = nw.s0, loads = 0;                   // first (`loads` even), then values
-        int armed = 0;                               // loads whose copies were issued
         uint32_t ld_at = 0;
         bool more = true;
         // Queries into L2, ahead of the rows' copies: they are read when the item begins.
@@ -313,7 +313,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                     ++ns;
                     continue;
                 }
-                if (lane == 0 && !late) {
+                if (lane == 0 && late < 0) {
                     const int row = ex_row(it.o, c0);
                     const uint32_t b = bar + ld_at * 8;
                     const CUtensorMap *map = it.b < 0 ? (loads & 1 ? &maps.pv : &maps.pk)
@@ -327,7 +327,6 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                 }
                 ns += loads & 1;
                 ++loads;
-                if (!late) armed = loads;
                 ld_at = ld_at + 1 == UNITS ? 0 : ld_at + 1;
                 return;
             }
@@ -340,7 +339,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
         x8.init();
         uint32_t unit = 0, parity = 0;
         auto full = [&]() {                          // the unit in use has arrived
-            if (!wait_for(bar + unit * 8, parity, late ? 0u : a.polls)) late = true;
+            if (late < 0 && !wait_for(bar + unit * 8, parity, a.polls)) late = loads;
         };
         auto taken = [&]() {                         // the unit in use is free: refill it
             __syncwarp();
@@ -704,10 +703,10 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
             if (parts > 1) cluster_sync();
             have = w.next(a, rs, rank, parts);
         }
-        if (late) {
+        if (late >= 0) {
             // copies still in flight end before the block does (bounded); the first lane has issued them
             atomicExch(&g_split_status, 1);
-            for (int i = max(0, armed - UNITS); lane == 0 && i < armed; ++i)
+            for (int i = max(0, late - UNITS); lane == 0 && i < late; ++i)
                 wait_for(bar + (i % UNITS) * 8, (i / UNITS) & 1, EX_POLLS);
         }
     }
