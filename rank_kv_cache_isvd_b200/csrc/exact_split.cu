@@ -298,6 +298,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                     (it.b < 0 ? 0 : i) * a.q_tok + line * 128));
         };
         bring_queries(nw.it);
+        uint64_t policy = l2_policy(nw.it.b >= 0);
         // Fills one unit of the ring with this warp's rows of the next step that has any.
         auto load = [&]() {
             while (more) {
@@ -306,6 +307,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                     if (!more) return;
                     ns = nw.s0;
                     bring_queries(nw.it);
+                    policy = l2_policy(nw.it.b >= 0);
                 }
                 const Item &it = nw.it;
                 const int c0 = ns * rs + tw * WR;
@@ -323,7 +325,7 @@ exact_split_kernel(const __grid_constant__ ExactArgs a, const __grid_constant__ 
                                  : "memory");
                     const int hd = it.h * (it.b < 0 ? a.p_head_mul : a.head_mul);
                     const int sq = it.b < 0 ? 0 : it.b * a.seq_mul;
-                    tma_load_5d_once(ring + ld_at * UNIT, map, row, hd, sq, b);
+                    tma_load_5d(ring + ld_at * UNIT, map, row, hd, sq, b, policy);
                 }
                 ns += loads & 1;
                 ++loads;

@@ -123,16 +123,24 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(0), "r"(head), "r"(seq), "r"(bar)
         : "memory");
 }
-// The same for rows that leave L2 before other data does. Decode reads a sequence's rows once, but
-// scores and records twice, and a shared prefix by every call (weights of 8 x 32768 rows: 187 -> 183 us,
-// 130 sequences behind a prefix of 4001: 67.5 -> 61.2 us, window of 4 x 65536: 19.1 -> 18.8 us).
-__device__ __forceinline__ void tma_load_5d_once(uint32_t dst, const CUtensorMap *map, int row,
-                                                 int head, int seq, uint32_t bar) {
+// L2's policy for rows. A decode reads a sequence's own rows once: they leave L2 first, before scores and
+// records, which are read twice (weights of 8 x 32768 rows: 187 -> 183 us, window of 4 x 65536: 19.1 -> 18.8),
+// and before a shared prefix, which the next call reads again (130 sequences behind a prefix of 4001:
+// 67.5 -> 61.2 us). The prefix itself stays as long as it can: with its rows first out as well, two sequences of
+// 8192 rows behind a prefix of 16384 took 40.7 us instead of 35.1.
+__device__ __forceinline__ uint64_t l2_policy(bool once) {
+    uint64_t p;
+    if (once) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, int row, int head, int seq,
+                                            uint32_t bar, uint64_t policy) {
     asm volatile(
-        "{\n\t.reg .b64 p;\n\tcreatepolicy.fractional.L2::evict_first.b64 p, 1.0;\n\t"
         "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], p;\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(0), "r"(head), "r"(seq), "r"(bar)
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(0), "r"(head), "r"(seq), "r"(bar),
+        "l"(policy)
         : "memory");
 }
 // False: the wait gave up.
