@@ -63,16 +63,22 @@ exact_rows_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
     }
     __syncthreads();
     int issued = 0;
-    bool late = false;                 // a wait of this lane gave up: it waits no more, and loads no more
+    // Once a wait of this lane has given up: how many loads were issued then (-1 before). It waits no more (no
+    // polls: a branch around each wait took up to 12 % of a call) and issues no more copies; what is left of
+    // the steps says nothing then.
+    int late = -1;
+    uint32_t polls = a.polls;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        const bool ok = wait_for(bar, parity, polls);
+        late = !ok && late < 0 ? issued : late;
+        polls = ok ? polls : 0u;
+    };
     // Unit u (keys and values of a step in turn), by warp 0 once all warps are done with its place.
     auto load = [&]() {
-        if (late || issued >= loads) return;
+        if (issued >= loads) return;
         const int at = issued % RING;
-        if (issued >= RING && !wait_for(empty + at * 8, (issued / RING + 1) & 1, a.polls)) {
-            late = true;
-            return;
-        }
-        if (lane == 0) {
+        if (issued >= RING) wait(empty + at * 8, (issued / RING + 1) & 1);
+        if (lane == 0 && late < 0) {
             const int row = ex_row(o, (s0 + issued / 2) * WR);
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full + at * 8),
                          "r"(UNIT)
@@ -104,9 +110,8 @@ exact_rows_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
         const int c0 = (s0 + u / 2) * WR;
         const int seen = ex_seen(o, c0, WR), row0 = ex_row(o, c0);
         const int ka = u % RING, va = (u + 1) % RING;
-        if (!late)
-            late = !wait_for(full + ka * 8, (u / RING) & 1, a.polls) ||
-                   !wait_for(full + va * 8, ((u + 1) / RING) & 1, a.polls);
+        wait(full + ka * 8, (u / RING) & 1);
+        wait(full + va * 8, ((u + 1) / RING) & 1);
         if (!PREFIX && seen < WR) {
             // values that no token of the group sees may be anything (the same steps in all warps)
             if (warp == 0) Rows::clear(ring + va * UNIT, seen);
@@ -172,11 +177,11 @@ exact_rows_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CU
             }
         }
     }
-    if (late) {
+    if (late >= 0) {
         // copies still in flight end before the block does (bounded); the first lane has issued them
         atomicExch(&g_rows_status, 1);
         if (warp == 0 && lane == 0)
-            for (int i = max(0, issued - RING); i < issued; ++i)
+            for (int i = max(0, late - RING); i < late; ++i)
                 wait_for(full + (i % RING) * 8, (i / RING) & 1, EX_POLLS);
     }
 }
