@@ -337,8 +337,13 @@ int iskv_decode_attn_noalloc(const iskv_decode_view *view, const float *q_dev, f
  * workspaces of their own; that goes for two captured graphs that are replayed at the same time.
  * They run on the current CUDA device, which has to own all the pointers, and are capturable.
  *
- * Keys are as attended (already rotated), scores have the scale 1/sqrt(128), the softmax is exact,
- * q-head g reads kv-head g / (n_q/n_kv), and a query that sees no row gives zeros. Rows that no
+ * Keys are as attended (already rotated), scores have the scale 1/sqrt(128), q-head g reads kv-head
+ * g / (n_q/n_kv), and a query that sees no row gives zeros. The softmax is over all rows that a query
+ * sees; maxima, sums and accumulators are float32. With float32 queries, products keep 22 bits and more.
+ * With bf16 queries, a call that has more than 8 query rows (tokens or sequences, times q-heads) for a
+ * kv-head's rows may round each softmax weight to bf16 before its product with the value (the sum of the
+ * weights takes them unrounded): outputs are then off by up to 1.41 times what rounding them to bf16
+ * alone gives. Others keep two bf16 terms of each weight. Rows that no
  * query of their sequence sees are not used: they may hold anything, NaN included. Device arrays
  * of lengths are read on the device: values below 0 count as 0, values above the capacity as the
  * capacity. Strides count elements and have to be multiples of 16 bytes; those of sequences, heads

@@ -334,8 +334,8 @@ void split_plan(ExactArgs &a, bool f32_rows, int sms) {
     a.by_items = 0;
     a.rt_max = tiles;
     // bf16 rows saturate HBM from fewer SMs than there are, and with more copies in flight it gives less
-    // (10 x 32768 rows of 8 kv-heads: 212 us on 148 SMs, 207 on 100; 150 x 2048, ragged: 171 and 162; with
-    // weights, 10 x 8192 ragged: 66 on 148 or 100, 62 on 120). Float32 rows are bound by instructions.
+    // (10 x 32768 rows of 8 kv-heads: 214 us on 148 SMs, 203 on 100; 150 x 2048, ragged: 174 and 162; with
+    // weights, 10 x 8192 ragged: 67 on 148, 63 on 120). Float32 rows are bound by instructions.
     auto by_steps = [&](int team) {
         a.grid = f32_rows || a.shared_here ? sms : a.mass ? sms - sms / 5 : sms - sms / 3;
         a.team = team;
@@ -357,10 +357,10 @@ void split_plan(ExactArgs &a, bool f32_rows, int sms) {
     if (c == 1) slots = (long long)sms * (EX_WARPS / team);
     const long long rounds = (items + slots - 1) / slots;
     // Long items that leave teams idle go by steps, which are shared out evenly but cost records and a
-    // merge. By items 10 x 8192 rows of 8 kv-heads take 53 us on 80 SMs, by steps 63: one round on half of
+    // merge. By items 10 x 8192 rows of 8 kv-heads take 53 us on 80 SMs, by steps 64: one round on half of
     // the SMs saturates HBM. But where lengths may differ (a list, read on the device) short items leave
-    // more idle: 19 x 8192, ragged, 98 and 80 us, in several rounds 150 x 2048 216 and 205, of float32 rows
-    // 75 x 2 x 4096 189 and 118. Of 16 steps, 40 x 1000 ragged, items take 30 us and steps 34.
+    // more idle: 19 x 8192, ragged, 98 and 81 us, in several rounds 150 x 2048 258 and 205, of float32 rows
+    // 75 x 2 x 4096 196 and 121. Of 16 steps, 40 x 1000 ragged, items take 30 us and steps 34.
     const bool idle = 4 * items < (f32_rows || a.lens || rounds > 1 ? 3 : 2) * rounds * slots;
     if (idle && steps > (f32_rows ? 8 : 16) * c) return by_steps(items >= 2 * sms ? 1 : EX_WARPS);
     const long long teams = items < slots ? items : slots;

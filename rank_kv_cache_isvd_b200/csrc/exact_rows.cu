@@ -5,10 +5,11 @@
 // tf32 products (exact_warp.cuh): 64 mma.sync per 32 keys and 8 rows, the bound of this kernel at
 // 145 TFLOP/s of float32 work. A CTA takes 64 query rows, 8 per warp, and all warps share one ring
 // of key and value units in shared memory. (The split kernel, which gives each tile of 8 rows its own
-// copy of the rows, was bound by L2 here: 950 us against 425 us at 94 x 4 queries of 8 kv-heads over
-// 7264 shared rows.) The same products reach 73 TFLOP/s (130 x 8 queries over 16384 shared rows:
-// 957 us); fetching and decoding instructions, then the splitting, take the rest. As in the tile
-// kernel a CTA does a split of the rows' steps where CTAs are few.
+// copy of the rows, was bound by L2 here: 950 us against 435 us at 94 x 4 queries of 8 kv-heads over
+// 7264 shared float32 rows.) They reach 73 TFLOP/s over bf16 rows (130 x 8 queries over 16384 shared
+// rows: 964 us) and 27 over float32 rows (a causal prompt of 4096: 5070 us, over bf16 rows 1785); fetching
+// and decoding instructions, then the splitting, take the rest. As in the tile kernel a CTA does a split
+// of the rows' steps where CTAs are few.
 #include <atomic>
 
 #include "exact_tile.cuh"

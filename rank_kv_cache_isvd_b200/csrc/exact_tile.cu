@@ -25,8 +25,11 @@
 // exactly enough: P is at most 256). Moving it rescales O in tensor memory, which the softmax warp
 // does itself: S of this block being complete says that the P V before it is too.
 //
-// P is rounded to bf16 (half a step, up to 2^-8 of a weight, at random over the keys);
-// the sum l takes the unrounded values, and all sums are float32.
+// P is rounded to bf16 (half a step, up to 2^-8 of a weight, at random over the keys): the product's
+// operands are of one type, and a second term of P would be half as many products again for an error of the size
+// that rounding the outputs makes anyway (2.1e-3 to 2.3e-3 against 64 bits, of which 1.6e-3 to 1.7e-3 are the
+// outputs' own; the two errors are independent and of one size, so 1.41 times at most). The sum l takes the
+// unrounded values, and all sums are float32.
 //
 // Every wait is bounded (iskv_exact_wait_limit). A wait that gives up sets the CTA's abort flag and the device's status
 // word; all roles then leave their loops, copies in flight are waited for, and tensor memory is
